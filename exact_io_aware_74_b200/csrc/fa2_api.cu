@@ -14,6 +14,7 @@
 #include "fa2_bwd.cuh"
 #include "fa2_decode.cuh"
 #include "fa2_fwd.cuh"
+#include "fa2_host.h"
 
 namespace {
 
@@ -177,6 +178,47 @@ bool make_acc_map(CUtensorMap* map, float* base, int BH, int N, int d) {
   const cuuint32_t box[3] = {32, 128, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---- services for the other translation units (fa2_host.h) ----
+
+int host_device(int* dev, int* n_sm, unsigned int** status) {
+  const int rc = check_device(dev);
+  if (rc != FA2_OK) return rc;
+  if (cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess ||
+      *n_sm <= 0) {
+    cudaGetLastError();
+    return FA2_ERR_CUDA;
+  }
+  *status = status_word(*dev);
+  return *status ? FA2_OK : FA2_ERR_CUDA;
+}
+
+unsigned long long host_wait_ns() {
+  return static_cast<unsigned long long>(g_wait_ms.load()) * 1000000ull;
+}
+int host_fault() { return g_fault.load(); }
+void host_count_launches(unsigned long long n) { g_launches.fetch_add(n); }
+
+bool host_encode_map(CUtensorMap* map, MapType type, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  cuuint64_t dm[5], st[5];
+  cuuint32_t bx[5];
+  for (int i = 0; i < rank; ++i) {
+    dm[i] = dims[i];
+    bx[i] = box[i];
+    st[i] = i + 1 < rank ? strides[i] : 0;
+  }
+  const CUtensorMapDataType ty = type == MapType::kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : type == MapType::kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dm, st, bx, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -99,7 +99,7 @@ struct WaitCtl {
 // Device status word layout: low 8 bits = status code, bits 8..15 = wait site.
 constexpr unsigned int kStatusTimeout = 5u;
 
-__device__ __noinline__ void report_timeout(const WaitCtl& w, uint32_t site) {
+static __device__ __noinline__ void report_timeout(const WaitCtl& w, uint32_t site) {
   *w.abort = 1;
   atomicCAS(w.status, 0u, kStatusTimeout | (site << 8));
 }

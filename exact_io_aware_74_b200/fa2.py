@@ -32,10 +32,24 @@ EXPORTS = ("fa2_fwd", "fa2_fwd_window", "fa2_fwd_fp8", "fa2_fwd_tiles_per_cta",
            "fa2_fwd_decode_splits", "fa2_fwd_decode_workspace_size", "fa2_fwd_decode",
            "fa2_bwd_workspace_size", "fa2_bwd", "fa2_bwd_window", "fa2_bwd_ex",
            "fa2_bwd_ex_workspace_size", "fa2_bwd_noalloc", "fa2_get_device_status",
-           "fa2_status_string", "fa2_debug_set", "fa2_debug_set_bwd_grid",
+           "fa2_fwd_varlen", "fa2_bwd_varlen_workspace_size", "fa2_bwd_varlen",
+           "fa2_fwd_paged_workspace_size", "fa2_fwd_paged", "fa2_paged_tables",
+           "fa2_paged_append", "fa2_status_string", "fa2_debug_set", "fa2_debug_set_bwd_grid",
            "fa2_debug_set_fwd_tiles", "fa2_launch_count")
 
 _lib = None
+
+
+class FA2Packed(ctypes.Structure):
+    """fa2_packed: a [T, heads, d] tensor by its address and strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_row", ctypes.c_longlong),
+                ("stride_head", ctypes.c_longlong)]
+
+
+class FA2Cache(ctypes.Structure):
+    """fa2_cache: a [blocks, heads, block_size, d] cache by its address and strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_block", ctypes.c_longlong),
+                ("stride_head", ctypes.c_longlong), ("stride_row", ctypes.c_longlong)]
 
 
 class FA2Error(RuntimeError):
@@ -80,6 +94,22 @@ def load() -> ctypes.CDLL:
     lib.fa2_bwd_ex_workspace_size.restype = sz
     lib.fa2_bwd_noalloc.argtypes = [vp] * 9 + [i, i, i, i, f, i, i, vp]
     lib.fa2_bwd_noalloc.restype = i
+    pk, pc = ctypes.POINTER(FA2Packed), ctypes.POINTER(FA2Cache)
+    lib.fa2_fwd_varlen.argtypes = [pk] * 4 + [vp, vp, i, i, i, i, i, f, i, i, i, vp]
+    lib.fa2_fwd_varlen.restype = i
+    lib.fa2_bwd_varlen_workspace_size.argtypes = [i] * 5
+    lib.fa2_bwd_varlen_workspace_size.restype = sz
+    lib.fa2_bwd_varlen.argtypes = [pk] * 5 + [vp] + [pk] * 3 + [vp, vp, sz, i, i, i, i, i, f, i, i,
+                                                               i, vp]
+    lib.fa2_bwd_varlen.restype = i
+    lib.fa2_fwd_paged_workspace_size.argtypes = [i] * 6
+    lib.fa2_fwd_paged_workspace_size.restype = sz
+    lib.fa2_fwd_paged.argtypes = [pk, pc, pc, pk] + [vp] * 5 + [sz] + [i] * 8 + [f, i, i, i, vp]
+    lib.fa2_fwd_paged.restype = i
+    lib.fa2_paged_tables.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, vp, i, i, i, i, vp]
+    lib.fa2_paged_tables.restype = i
+    lib.fa2_paged_append.argtypes = [pk, pk, pc, pc, vp, i, i, i, i, i, vp]
+    lib.fa2_paged_append.restype = i
     lib.fa2_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     lib.fa2_get_device_status.restype = i
     lib.fa2_status_string.argtypes = [i]
@@ -239,6 +269,191 @@ def fa2_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, scale: float, causal: bool,
                                   int(bool(causal)), _dtype_code(q), _stream(stream))
 
 
+# ------------------------------------------------------------------------------------
+# packed sequences, grouped heads and paged caches
+# ------------------------------------------------------------------------------------
+
+def _check_rows(dtype, *ts) -> None:
+    """[T, heads, d] tensors of one 16-bit dtype on one device, columns contiguous."""
+    dev = ts[0].device
+    for t in ts:
+        if t.dim() != 3 or not t.is_cuda or t.dtype != dtype or t.device != dev:
+            raise ValueError("packed tensors must be [T, heads, d] CUDA tensors of one dtype "
+                             "on one device")
+        if t.stride(2) != 1 and t.shape[2] != 1:
+            raise ValueError("the columns of a packed tensor must be contiguous")
+
+
+def _check_ints(device, **ts) -> None:
+    for name, t in ts.items():
+        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+
+
+def _packed(t) -> FA2Packed:
+    row, head, _ = t.stride()
+    return FA2Packed(t.data_ptr(), row, head)
+
+
+def _cache(t) -> FA2Cache:
+    block, head, row, _ = t.stride()
+    return FA2Cache(t.data_ptr(), block, head, row)
+
+
+class _on:
+    """Makes ``device`` current for a call (the library works on the current device)."""
+    __slots__ = ("idx", "old")
+
+    def __init__(self, device):
+        self.idx = device.index
+
+    def __enter__(self):
+        self.old = torch.cuda.current_device()
+        if self.old != self.idx:
+            torch.cuda.set_device(self.idx)
+
+    def __exit__(self, *exc):
+        if self.old != self.idx:
+            torch.cuda.set_device(self.old)
+
+
+def _check_lse(lse, H: int, T: int, device) -> None:
+    if lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous() or \
+            lse.device != device:
+        raise ValueError(f"lse must be a contiguous float32 [{H}, {T}] tensor on {device}")
+
+
+def _same_shape(shape, **ts) -> None:
+    for name, t in ts.items():
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def fa2_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale: float, causal: bool, window: int = 0,
+                   stream=None) -> int:
+    """Raw call: q, o [T,H,d] and k, v [T,Hkv,d] 16-bit, any row and head strides that are
+    multiples of 8; lse [H,T] float32; cu_seqlens [B+1] int32.  Returns the status."""
+    _check_rows(q.dtype, q, k, v, o)
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    _same_shape((T, Hkv, d), k=k, v=v)
+    _same_shape(q.shape, o=o)
+    _check_lse(lse, H, T, q.device)
+    _check_ints(q.device, cu_seqlens=cu_seqlens)
+    with _on(q.device):
+        return load().fa2_fwd_varlen(_packed(q), _packed(k), _packed(v), _packed(o), lse.data_ptr(),
+                                     cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T, H, Hkv, d,
+                                     scale, int(bool(causal)), int(window), _dtype_code(q),
+                                     _stream(stream))
+
+
+def fa2_bwd_varlen_workspace_size(B: int, T: int, H: int, Hkv: int, d: int) -> int:
+    return int(load().fa2_bwd_varlen_workspace_size(B, T, H, Hkv, d))
+
+
+def fa2_bwd_varlen(q, k, v, o, do, lse, dq, dk, dv, cu_seqlens, workspace, scale: float,
+                   causal: bool, window: int = 0, stream=None) -> int:
+    """Raw call of the packed backward; ``workspace`` is a uint8 CUDA tensor."""
+    _check_rows(q.dtype, q, k, v, o, do, dq, dk, dv)
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    _same_shape((T, Hkv, d), k=k, v=v, dk=dk, dv=dv)
+    _same_shape(q.shape, o=o, do=do, dq=dq)
+    _check_lse(lse, H, T, q.device)
+    _check_ints(q.device, cu_seqlens=cu_seqlens)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(q.device):
+        return load().fa2_bwd_varlen(_packed(q), _packed(k), _packed(v), _packed(o), _packed(do),
+                                     lse.data_ptr(), _packed(dq), _packed(dk), _packed(dv),
+                                     cu_seqlens.data_ptr(), _ptr(workspace), ws_bytes,
+                                     cu_seqlens.numel() - 1, T, H, Hkv, d, scale,
+                                     int(bool(causal)), int(window), _dtype_code(q),
+                                     _stream(stream))
+
+
+def _check_caches(*cs) -> None:
+    for c in cs:
+        if c.dim() != 4 or not c.is_cuda or (c.stride(3) != 1 and c.shape[3] != 1):
+            raise ValueError("caches must be [blocks, heads, block_size, d] CUDA tensors with "
+                             "contiguous columns")
+
+
+def fa2_fwd_paged_workspace_size(B: int, T: int, H: int, Hkv: int, d: int,
+                                 sm_count: int = 0) -> int:
+    return int(load().fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, sm_count))
+
+
+def fa2_fwd_paged(q, k_cache, v_cache, o, lse, block_table, cu_seqlens, seq_lens, workspace,
+                  scale: float, causal: bool, window: int = 0, stream=None) -> int:
+    """Raw call: q, o [T,H,d]; caches [blocks,Hkv,block_size,d]; lse [H,T] float32;
+    block_table [B,max_blocks], cu_seqlens [B+1], seq_lens [B] int32."""
+    _check_rows(q.dtype, q, o)
+    _check_caches(k_cache, v_cache)
+    T, H, d = q.shape
+    blocks, Hkv, bs, _ = k_cache.shape
+    _same_shape((blocks, Hkv, bs, d), k_cache=k_cache, v_cache=v_cache)
+    _same_shape(q.shape, o=o)
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or k_cache.device != q.device or \
+            v_cache.device != q.device:
+        raise ValueError("caches must have the queries' dtype and device")
+    B, max_blocks = block_table.shape
+    _same_shape((B,), seq_lens=seq_lens)
+    _same_shape((B + 1,), cu_seqlens=cu_seqlens)
+    _check_lse(lse, H, T, q.device)
+    _check_ints(q.device, block_table=block_table, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(q.device):
+        return load().fa2_fwd_paged(_packed(q), _cache(k_cache), _cache(v_cache), _packed(o),
+                                    lse.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+                                    block_table.data_ptr(), _ptr(workspace), ws_bytes, B, T, H,
+                                    Hkv, d, blocks, bs, max_blocks, scale, int(bool(causal)),
+                                    int(window), _dtype_code(q), _stream(stream))
+
+
+def fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu_seqlens, seq_lens,
+                     positions, slots, used, block_size: int, stream=None) -> int:
+    """Raw call: int32 tensors, context_lens and new_lens [B], free_blocks [num_free],
+    block_table [B,max_blocks] (updated), cu_seqlens [B+1], seq_lens [B], positions and
+    slots [T], used [1]."""
+    _check_ints(context_lens.device, context_lens=context_lens, new_lens=new_lens,
+                free_blocks=free_blocks, block_table=block_table, cu_seqlens=cu_seqlens,
+                seq_lens=seq_lens, positions=positions, slots=slots, used=used)
+    if not context_lens.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    B, max_blocks = block_table.shape
+    T = slots.numel()
+    _same_shape((B,), context_lens=context_lens, new_lens=new_lens, seq_lens=seq_lens)
+    _same_shape((B + 1,), cu_seqlens=cu_seqlens)
+    _same_shape((T,), positions=positions, slots=slots)
+    _same_shape((1,), used=used)
+    with _on(context_lens.device):
+        return load().fa2_paged_tables(context_lens.data_ptr(), new_lens.data_ptr(),
+                                       free_blocks.data_ptr(), free_blocks.numel(),
+                                       block_table.data_ptr(), cu_seqlens.data_ptr(),
+                                       seq_lens.data_ptr(), positions.data_ptr(),
+                                       slots.data_ptr(), used.data_ptr(), B, T, int(block_size),
+                                       max_blocks, _stream(stream))
+
+
+def fa2_paged_append(k, v, k_cache, v_cache, slots, stream=None) -> int:
+    """Raw call: k, v [T,Hkv,d], caches [blocks,Hkv,block_size,d], slots [T] int32."""
+    _check_rows(k.dtype, k, v)
+    _check_caches(k_cache, v_cache)
+    _dtype_code(k)
+    T, Hkv, d = k.shape
+    blocks, _, bs, _ = k_cache.shape
+    _same_shape(k.shape, v=v)
+    _same_shape((blocks, Hkv, bs, d), k_cache=k_cache, v_cache=v_cache)
+    _same_shape((T,), slots=slots)
+    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype or k_cache.device != k.device or \
+            v_cache.device != k.device:
+        raise ValueError("caches must have the dtype and device of k and v")
+    _check_ints(k.device, slots=slots)
+    with _on(k.device):
+        return load().fa2_paged_append(_packed(k), _packed(v), _cache(k_cache), _cache(v_cache),
+                                       slots.data_ptr(), T, Hkv, d, blocks, bs, _stream(stream))
+
+
 def fa2_get_device_status(stream=None) -> tuple[int, int]:
     """(status, wait site) of the current device; synchronises ``stream``."""
     site = ctypes.c_int(0)
@@ -355,3 +570,78 @@ def backward(q, k, v, o, do, lse, scale: float, causal: bool, workspace=None, st
     if rc != FA2_OK:
         raise FA2Error(rc, where)
     return dq, dk, dv
+
+
+def forward_varlen(q, k, v, cu_seqlens, scale: float, causal: bool, window: int = 0, stream=None):
+    """Attention over packed sequences: O [T,H,d] and LSE [H,T] of q [T,H,d] and k, v
+    [T,Hkv,d], sequence b being rows cu_seqlens[b] .. cu_seqlens[b+1] - 1.  Rows behind
+    the last sequence are not written (fa2_fwd_varlen takes outputs of your own)."""
+    T, H, d = q.shape
+    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    rc = fa2_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, window, stream)
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_fwd_varlen")
+    return o, lse
+
+
+def backward_varlen(q, k, v, o, do, lse, cu_seqlens, scale: float, causal: bool, window: int = 0,
+                    workspace=None, stream=None):
+    """Gradients dQ [T,H,d], dK and dV [T,Hkv,d] of forward_varlen; the workspace is
+    allocated if not given."""
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    if workspace is None:
+        n = fa2_bwd_varlen_workspace_size(cu_seqlens.numel() - 1, T, H, Hkv, d)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    dq = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    dk = torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device)
+    dv = torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device)
+    rc = fa2_bwd_varlen(q, k, v, o, do, lse, dq, dk, dv, cu_seqlens, workspace, scale, causal,
+                        window, stream)
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_bwd_varlen")
+    return dq, dk, dv
+
+
+def forward_paged(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scale: float,
+                  causal: bool, window: int = 0, workspace=None, stream=None):
+    """Attention of a step's new tokens q [T,H,d] over paged caches
+    [blocks,Hkv,block_size,d]: O [T,H,d] and LSE [H,T].  The workspace is allocated if
+    not given."""
+    T, H, d = q.shape
+    if workspace is None:
+        with _on(q.device):
+            n = fa2_fwd_paged_workspace_size(block_table.shape[0], T, H, k_cache.shape[1], d)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    rc = fa2_fwd_paged(q, k_cache, v_cache, o, lse, block_table, cu_seqlens, seq_lens, workspace,
+                       scale, causal, window, stream)
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_fwd_paged")
+    return o, lse
+
+
+def paged_tables(context_lens, new_lens, free_blocks, block_table, T: int, block_size: int,
+                 stream=None):
+    """Tables of a step of at most T new tokens: (block_table, updated in place,
+    cu_seqlens [B+1], seq_lens [B], positions [T], slots [T], used [1])."""
+    B = block_table.shape[0]
+    ints = dict(dtype=torch.int32, device=block_table.device)
+    cu, lens = torch.empty(B + 1, **ints), torch.empty(B, **ints)
+    positions, slots = torch.empty(T, **ints), torch.empty(T, **ints)
+    used = torch.empty(1, **ints)
+    rc = fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu, lens, positions,
+                          slots, used, block_size, stream)
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_paged_tables")
+    return block_table, cu, lens, positions, slots, used
+
+
+def paged_append(k, v, k_cache, v_cache, slots, stream=None):
+    """Writes k, v [T,Hkv,d] into the caches by slot; returns the caches."""
+    rc = fa2_paged_append(k, v, k_cache, v_cache, slots, stream)
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_paged_append")
+    return k_cache, v_cache

@@ -56,7 +56,8 @@ typedef struct CUstream_st* fa2_stream_t;
 
 typedef enum {
   FA2_OK = 0,
-  FA2_ERR_INVALID_ARG = 1, /* null / misaligned pointer, bad size, flag or scale */
+  FA2_ERR_INVALID_ARG = 1, /* null / misaligned pointer, bad size, flag or scale; as a
+                              device status: a block or slot outside the cache */
   FA2_ERR_UNSUPPORTED = 2, /* head dim the call does not support */
   FA2_ERR_ARCH = 3,        /* current device is not compute capability 10.0 */
   FA2_ERR_CUDA = 4,        /* a CUDA runtime / driver call failed */
@@ -278,6 +279,160 @@ size_t fa2_bwd_ex_workspace_size(int B, int H, int N, int d, int flags);
 int fa2_bwd_noalloc(const void* Q, const void* K, const void* V, const void* O, const void* dO,
                     const float* LSE, void* dQ, void* dK, void* dV, int B, int H, int N, int d,
                     float scale, int causal, int dtype, fa2_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Packed sequences, grouped heads and paged caches
+ *
+ * A batch of B sequences of different lengths lies packed, one after the other, in
+ * tensors of T rows (tokens): sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+ * (cu_seqlens is B + 1 int, on the device, cu_seqlens[0] = 0, not decreasing).  The
+ * lengths stay on the device: nothing reads them back, and a captured call follows
+ * them when it is replayed.  Sequences may be empty.  Rows from cu_seqlens[B] to T - 1
+ * belong to no sequence; they are not computed, and outputs there are left as they
+ * were.  Offsets outside 0 .. T are clamped, so that no bad value reads or writes
+ * outside the tensors; the results of a batch with such offsets are unspecified.
+ *
+ * Grouped heads: H query heads share Hkv key/value heads, H a multiple of Hkv with at
+ * most 128 query heads to one of them; query head h reads key/value head h / (H / Hkv).
+ * ---------------------------------------------------------------------------------- */
+
+/* A packed 16-bit tensor: element (row r, head h, column c) is at
+ * data + r * stride_row + h * stride_head + c, strides in elements.  Strides are
+ * multiples of 8 and at least the head dim, data is 16-byte aligned; a slice of a wider
+ * projection and a head-major tensor are both of this form. */
+typedef struct {
+  void* data;
+  long long stride_row;
+  long long stride_head;
+} fa2_packed;
+
+/* A paged 16-bit cache: block p holds block_size consecutive positions of one sequence
+ * for every key/value head; element (p, h, position, column c) is at
+ * data + p * stride_block + h * stride_head + position * stride_row + c.  Strides as
+ * above.  Keys and values may lie interleaved in one allocation. */
+typedef struct {
+  void* data;
+  long long stride_block;
+  long long stride_head;
+  long long stride_row;
+} fa2_cache;
+
+/*
+ * Forward over packed sequences: every row attends to the rows of its own sequence,
+ * as fa2_fwd (window = 0) or fa2_fwd_window (window >= 1, causal = 1) would with each
+ * sequence alone.  Source: [DC] "Tiling".
+ *
+ *   Q, O       : [T] x H heads of d columns (in, out)
+ *   K, V       : [T] x Hkv heads of d columns (in)
+ *   LSE        : out, [H][T] float
+ *   cu_seqlens : in, [B + 1] int
+ *   T          : >= 0 (0 launches nothing); d a multiple of 8 up to 256
+ *   window     : 0, or >= 1 with causal = 1
+ * What lies in the tensors outside the sequences (NaN included) does not reach them.
+ * O and LSE must not overlap the inputs (FA2_ERR_INVALID_ARG when O or LSE start inside
+ * one).  Results are bitwise repeatable.
+ */
+int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V,
+                   const fa2_packed* O, float* LSE, const int* cu_seqlens, int B, int T, int H,
+                   int Hkv, int d, float scale, int causal, int window, int dtype,
+                   fa2_stream_t stream);
+
+/* Bytes of device workspace fa2_bwd_varlen needs, a multiple of 256; 0 for sizes it
+ * rejects. */
+size_t fa2_bwd_varlen_workspace_size(int B, int T, int H, int Hkv, int d);
+
+/*
+ * Backward of fa2_fwd_varlen.  [DC] "Ricomputazione"; dK and dV of a key/value head sum
+ * over the query heads that share it.
+ *
+ *   Q, O, dO, dQ  : [T] x H heads; K, V, dK, dV : [T] x Hkv heads (dQ, dK, dV out)
+ *   LSE           : in, [H][T] float, as fa2_fwd_varlen wrote it
+ *   d             : a multiple of 8 up to 128
+ *   workspace     : at least fa2_bwd_varlen_workspace_size() bytes, 256-byte aligned;
+ *                   its contents on entry do not matter
+ * Other arguments as for the forward.  Rows behind the last sequence are left as they
+ * were.  dQ may differ in the last bits from run to run (float atomics); dK and dV are
+ * repeatable.
+ */
+int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V,
+                   const fa2_packed* O, const fa2_packed* dO, const float* LSE,
+                   const fa2_packed* dQ, const fa2_packed* dK, const fa2_packed* dV,
+                   const int* cu_seqlens, void* workspace, size_t workspace_bytes, int B, int T,
+                   int H, int Hkv, int d, float scale, int causal, int window, int dtype,
+                   fa2_stream_t stream);
+
+/* Bytes of device workspace fa2_fwd_paged needs on a GPU with ``sm_count`` SMs (<= 0:
+ * the current device), a multiple of 256; 0 for sizes it rejects or when no device can
+ * be asked. */
+size_t fa2_fwd_paged_workspace_size(int B, int T, int H, int Hkv, int d, int sm_count);
+
+/*
+ * Attention of a step's new tokens over a paged cache: a whole prompt, a chunk of one,
+ * or single tokens (decode), mixed at will.  The rows of request b (cu_seqlens, as
+ * above) are the last positions of a sequence of seq_lens[b] keys, its new tokens
+ * included: they must be in the cache already (fa2_paged_append).  Row i of n sees keys
+ * 0 .. seq_lens[b] - n + i when causal (its last ``window`` of them with a window),
+ * every key otherwise.  A row that sees no key gets O = 0 and LSE = -inf.
+ * Source: [DC] "Parallelismo lungo la lunghezza della sequenza" (the keys are split
+ * where there are few rows).
+ *
+ *   Q, O        : [T] x H heads (in, out); LSE : out, [H][T] float
+ *   K, V        : in, caches of num_blocks blocks of block_size positions; block_size
+ *                 is 8, 16, 32, 64 or a multiple of 128
+ *   cu_seqlens  : in, [B + 1] int; seq_lens : in, [B] int, clamped to 0 .. max_blocks *
+ *                 block_size
+ *   block_table : in, [B][max_blocks] int: position j of request b is in block
+ *                 block_table[b][j / block_size].  Only entries that a visible key
+ *                 needs are read.  An entry outside 0 .. num_blocks - 1 reads as a
+ *                 block of zeros and reports FA2_ERR_INVALID_ARG through
+ *                 fa2_get_device_status.
+ *   workspace   : at least fa2_fwd_paged_workspace_size() bytes, 256-byte aligned, not
+ *                 shared with a call that may run at the same time
+ * Cache positions from seq_lens[b] on may hold anything, NaN included.  d a multiple of
+ * 8 up to 256.  Results are bitwise repeatable on one GPU.
+ */
+int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, const fa2_packed* O,
+                  float* LSE, const int* cu_seqlens, const int* seq_lens, const int* block_table,
+                  void* workspace, size_t workspace_bytes, int B, int T, int H, int Hkv, int d,
+                  int num_blocks, int block_size, int max_blocks, float scale, int causal,
+                  int window, int dtype, fa2_stream_t stream);
+
+/*
+ * Tables of a step, from the requests' lengths.  Request b has context_lens[b] tokens in
+ * the cache and brings new_lens[b] more (negative lengths count as 0).  It holds the
+ * blocks of its cached tokens in block_table[b]; the further blocks that its new tokens
+ * need are taken from free_blocks in order, request by request.
+ *
+ *   context_lens, new_lens : in, [B] int;  free_blocks : in, [num_free] int (not changed)
+ *   block_table : in and out, [B][max_blocks] int; only the new entries are written
+ *   cu_seqlens  : out, [B + 1] int, sums of new_lens
+ *   seq_lens    : out, [B] int, context_lens + new_lens
+ *   positions   : out, [T] int, position of each new token in its sequence
+ *   slots       : out, [T] int, block * block_size + offset in the block
+ *   used        : out, [1] int, blocks that the step needs.  More than num_free: the
+ *                 list ran out; the entries it could not serve are -1
+ * T is the room in positions and slots: entries past the step's tokens are position 0
+ * and slot -1, and tokens past T get neither.  A token whose block is missing (the list
+ * ran out, or max_blocks is too small) has slot -1.  B >= 1, T >= 0, num_free >= 0,
+ * block_size and max_blocks >= 1; the sums must stay below 2^31.  The outputs must not
+ * overlap the inputs or one another.
+ */
+int fa2_paged_tables(const int* context_lens, const int* new_lens, const int* free_blocks,
+                     int num_free, int* block_table, int* cu_seqlens, int* seq_lens,
+                     int* positions, int* slots, int* used, int B, int T, int block_size,
+                     int max_blocks, fa2_stream_t stream);
+
+/*
+ * Writes a step's keys and values into the paged cache: row t of K and V (T rows of Hkv
+ * heads) goes to position slots[t] % block_size of block slots[t] / block_size.  Rows
+ * with a negative slot are skipped, as are slots past the cache, which report
+ * FA2_ERR_INVALID_ARG through fa2_get_device_status.  Slots must differ from one
+ * another.  d a multiple of 8 up to 256, any block_size >= 1, 16-bit elements of either
+ * type; the caches must not overlap K and V.
+ */
+int fa2_paged_append(const fa2_packed* K, const fa2_packed* V, const fa2_cache* K_cache,
+                     const fa2_cache* V_cache, const int* slots, int T, int Hkv, int d,
+                     int num_blocks, int block_size, fa2_stream_t stream);
 
 /*
  * Synchronises ``stream``, then returns and clears the current device's status

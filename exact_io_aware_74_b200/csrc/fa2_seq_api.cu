@@ -4,12 +4,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/fa2.h"
 #include "fa2_host.h"
 #include "fa2_paged.cuh"
+#include "fa2_seq_fwd.cuh"
 #include "fa2_varlen.cuh"
 
 namespace {
@@ -51,8 +53,132 @@ bool cache_ok(const fa2_cache* x, int blocks, int heads, int rows, int d) {
 fa2::Packed packed(const fa2_packed* x) {
   return {static_cast<uint16_t*>(x->data), x->stride_row, x->stride_head};
 }
-fa2::Cache cache(const fa2_cache* x) {
-  return {static_cast<const uint16_t*>(x->data), x->stride_block, x->stride_head, x->stride_row};
+// ---- forward over packed sequences and paged caches ----
+
+int fwd_tile_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
+
+constexpr int kDevices = 64;
+
+template <typename Kern>
+bool set_smem_once(Kern kern, int dev, int smem, std::atomic<bool> (&done)[kDevices]) {
+  if (dev < 0 || dev >= kDevices) return false;
+  if (done[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+struct SeqMaps {
+  CUtensorMap q, k, v;
+};
+
+template <int D, bool BF16, int QT>
+int launch_seq(const SeqMaps& m, const fa2::SeqParams& p, int dev, unsigned int grid, cudaStream_t stream) {
+  using Cfg = fa2::SeqCfg<D, QT>;
+  auto kern = fa2::fa2_seq_fwd_kernel<D, BF16, QT>;
+  // The kernel re-splits its registers between warpgroups: only sound when every thread
+  // was launched with exactly LAUNCH_REGS of them.
+  static const bool regs_ok = [&] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs == Cfg::LAUNCH_REGS;
+  }();
+  static std::atomic<bool> smem_set[kDevices];
+  if (!regs_ok || !set_smem_once(kern, dev, Cfg::SMEM, smem_set)) {
+    cudaGetLastError();
+    return FA2_ERR_CUDA;
+  }
+  kern<<<grid, Cfg::THREADS, Cfg::SMEM, stream>>>(m.q, m.k, m.v, p);
+  if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
+  fa2::host_count_launches(1);
+  if (!p.block_table || grid < 2) return FA2_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid - 1, QT == 1 ? 2 : 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fa2::fa2_seq_merge_kernel<D, BF16, QT>, p, static_cast<int>(grid)) != cudaSuccess) {
+    cudaGetLastError();
+    return FA2_ERR_CUDA;
+  }
+  fa2::host_count_launches(1);
+  return FA2_OK;
+}
+
+int launch_seq_any(int d, bool bf, int qt, const SeqMaps& m, const fa2::SeqParams& p, int dev, unsigned int grid,
+                   cudaStream_t s) {
+#define FA2_SEQ(D_, QT_) return bf ? launch_seq<D_, true, QT_>(m, p, dev, grid, s) : launch_seq<D_, false, QT_>(m, p, dev, grid, s)
+  switch (fwd_tile_dim(d)) {
+    case 64: if (qt == 2) { FA2_SEQ(64, 2); } FA2_SEQ(64, 1);
+    case 128: if (qt == 2) { FA2_SEQ(128, 2); } FA2_SEQ(128, 1);
+    case 192: FA2_SEQ(192, 1);
+    default: FA2_SEQ(256, 1);
+  }
+#undef FA2_SEQ
+}
+
+// [T][heads][d] as a 3-D map (column, head, row) or (column, row, head).  The stride of
+// an axis with one entry is not the caller's.
+bool map_packed(CUtensorMap* m, const fa2_packed* x, int T, int heads, int d, int dtype, bool rows_inside,
+                uint32_t box_rows, uint32_t box_heads) {
+  const uint64_t row = T > 1 ? x->stride_row * 2 : d * 2, head = heads > 1 ? x->stride_head * 2 : d * 2;
+  const fa2::MapType ty = dtype == FA2_BF16 ? fa2::MapType::kBF16 : fa2::MapType::kF16;
+  const uint64_t D = d, N = T, H = heads;
+  if (rows_inside) {
+    const uint64_t dims[3] = {D, N, H}, strides[2] = {row, head};
+    const uint32_t box[3] = {64, box_rows, box_heads};
+    return fa2::host_encode_map(m, ty, x->data, 3, dims, strides, box);
+  }
+  const uint64_t dims[3] = {D, H, N}, strides[2] = {head, row};
+  const uint32_t box[3] = {64, box_heads, box_rows};
+  return fa2::host_encode_map(m, ty, x->data, 3, dims, strides, box);
+}
+
+bool map_cache(CUtensorMap* m, const fa2_cache* x, int blocks, int heads, int rows, int d, int dtype) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(heads),
+                            static_cast<uint64_t>(blocks)};
+  const uint64_t any = static_cast<uint64_t>(d) * 2;
+  const uint64_t strides[3] = {rows > 1 ? static_cast<uint64_t>(x->stride_row) * 2 : any,
+                               heads > 1 ? static_cast<uint64_t>(x->stride_head) * 2 : any,
+                               blocks > 1 ? static_cast<uint64_t>(x->stride_block) * 2 : any};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(std::min(rows, 128)), 1, 1};
+  return fa2::host_encode_map(m, dtype == FA2_BF16 ? fa2::MapType::kBF16 : fa2::MapType::kF16, x->data, 4, dims,
+                              strides, box);
+}
+
+fa2::SeqParams seq_params(const fa2_packed* O, float* LSE, const int* cu, unsigned int* st, int B, int T, int H,
+                          int Hkv, int d, float scale, int causal, int window) {
+  fa2::SeqParams p{};
+  p.O = static_cast<uint16_t*>(O->data);
+  p.o_row = O->stride_row;
+  p.o_head = O->stride_head;
+  p.LSE = LSE;
+  p.cu = cu;
+  p.status = st;
+  p.wait_ns = fa2::host_wait_ns();
+  p.fault = fa2::host_fault();
+  p.B = B, p.T = T, p.Hkv = Hkv, p.G = H / Hkv, p.d = d, p.tpt = 128 / p.G;
+  p.causal = causal, p.window = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return p;
+}
+
+// Query tiles of a paged item: two where the requests bring more than a tile of rows on
+// average (prompts, chunks), one for decode steps, whose second tile would be empty.
+int paged_tiles(int B, int T, int G, int d) { return d <= 128 && T > static_cast<long long>(128 / G) * B ? 2 : 1; }
+
+// Float partials of the shares: two slots each, O then LSE.
+size_t paged_opart_bytes(int grid, int qt, int d) {
+  return static_cast<size_t>(grid) * 2 * qt * 128 * fwd_tile_dim(d) * 4;
+}
+size_t paged_bytes(int grid, int qt, int d) {
+  return paged_opart_bytes(grid, qt, d) + static_cast<size_t>(grid) * 2 * qt * 128 * 4;
 }
 
 }  // namespace
@@ -76,23 +202,23 @@ int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   unsigned int* st;
   rc = fa2::host_device(&dev, &n_sm, &st);
   if (rc != FA2_OK) return rc;
-  fa2::VarlenParams p{};
-  p.Q = packed(Q);
-  p.K = packed(K);
-  p.V = packed(V);
-  p.O = packed(O);
-  p.LSE = LSE;
-  p.cu = cu_seqlens;
-  p.status = st;
-  p.B = B, p.T = T, p.H = H, p.Hkv = Hkv, p.d = d, p.causal = causal, p.window = window;
-  p.scale = scale;
-  const dim3 grid((T + 3) / 4, H);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == FA2_BF16) fa2::fa2_varlen_fwd_plain<true, false><<<grid, 128, 0, s>>>(p);
-  else fa2::fa2_varlen_fwd_plain<false, false><<<grid, 128, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
-  fa2::host_count_launches(1);
-  return FA2_OK;
+  const int G = H / Hkv, tpt = 128 / G;
+  // Items there could be: every sequence's last block may be partial.
+  const auto items = [&](int qt) {
+    return (static_cast<long long>(T) / (qt * tpt) + std::min(B, T)) * Hkv;
+  };
+  // Two query tiles to a CTA; one (twice the CTAs) where two would leave SMs without work.
+  const int qt = d <= 128 && items(2) >= n_sm ? 2 : 1;
+  if (items(qt) > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
+  SeqMaps m;
+  if (!map_packed(&m.q, Q, T, H, d, dtype, false, tpt, G) || !map_packed(&m.k, K, T, Hkv, d, dtype, true, 128, 1) ||
+      !map_packed(&m.v, V, T, Hkv, d, dtype, true, 128, 1))
+    return FA2_ERR_CUDA;
+  fa2::SeqParams p = seq_params(O, LSE, cu_seqlens, st, B, T, H, Hkv, d, scale, causal, window);
+  const long long per_head = items(qt) / Hkv;
+  p.head_group = static_cast<int>(std::min<long long>(Hkv, std::max<long long>(1, (2LL * n_sm + per_head - 1) / per_head)));
+  return launch_seq_any(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(items(qt)),
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t fa2_bwd_varlen_workspace_size(int B, int T, int H, int Hkv, int d) {
@@ -166,7 +292,7 @@ size_t fa2_fwd_paged_workspace_size(int B, int T, int H, int Hkv, int d, int sm_
       return 0;
     }
   }
-  return 256;
+  return (paged_bytes(sm_count, paged_tiles(B, T, H / Hkv, d), d) + 255) / 256 * 256;
 }
 
 int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, const fa2_packed* O,
@@ -200,26 +326,21 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, n_sm))
     return FA2_ERR_WORKSPACE;
-  fa2::VarlenParams p{};
-  p.Q = packed(Q);
-  p.Kc = cache(K);
-  p.Vc = cache(V);
-  p.O = packed(O);
-  p.LSE = LSE;
-  p.cu = cu_seqlens;
+  const int G = H / Hkv, qt = paged_tiles(B, T, G, d);
+  SeqMaps m;
+  if (!map_packed(&m.q, Q, T, H, d, dtype, false, 128 / G, G) ||
+      !map_cache(&m.k, K, num_blocks, Hkv, block_size, d, dtype) ||
+      !map_cache(&m.v, V, num_blocks, Hkv, block_size, d, dtype))
+    return FA2_ERR_CUDA;
+  fa2::SeqParams p = seq_params(O, LSE, cu_seqlens, st, B, T, H, Hkv, d, scale, causal, window);
   p.seq_lens = seq_lens;
   p.block_table = block_table;
-  p.status = st;
-  p.B = B, p.T = T, p.H = H, p.Hkv = Hkv, p.d = d, p.causal = causal, p.window = window;
   p.num_blocks = num_blocks, p.block_size = block_size, p.max_blocks = max_blocks;
-  p.scale = scale;
-  const dim3 grid((T + 3) / 4, H);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == FA2_BF16) fa2::fa2_varlen_fwd_plain<true, true><<<grid, 128, 0, s>>>(p);
-  else fa2::fa2_varlen_fwd_plain<false, true><<<grid, 128, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
-  fa2::host_count_launches(1);
-  return FA2_OK;
+  p.box_rows = std::min(block_size, 128);
+  p.O_part = static_cast<float*>(workspace);
+  p.LSE_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_opart_bytes(n_sm, qt, d));
+  return launch_seq_any(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(n_sm),
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 int fa2_paged_tables(const int* context_lens, const int* new_lens, const int* free_blocks,

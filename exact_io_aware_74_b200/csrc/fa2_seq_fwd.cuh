@@ -1,0 +1,1098 @@
+// Forward attention over packed sequences and over paged caches, with grouped heads.
+//
+// The tiles, the online softmax and the products are those of the dense forward
+// (fa2_fwd.cuh): 128 x 128 score tiles in tensor memory, one thread to a score row, P
+// back to tensor memory for P V, the lazy rescale.  What differs:
+//
+// Rows.  A query tile holds the G = H / Hkv query heads of one key/value head: row
+// r = token * G + head, 128 / G tokens to a tile.  The K and V of a tile are then read
+// once for all the heads that share them, and a single token still fills G rows.
+//
+// Items.  An item is one (sequence, key/value head, QT tiles of rows) and a range of
+// key tiles.  The lengths are on the device, so the items are found there:
+//   packed:  the grid has one CTA for every item there could be (T / rows + B, times
+//            heads); a running CTA takes over the items of CTAs that have not started
+//            (cluster launch control), so that the hardware's block scheduler hands out
+//            the items in order of their index, heaviest first, and no counter in
+//            memory is needed.
+//   paged:   the key tiles of all items, end to end, are cut into equal shares, one per
+//            CTA.  An item that is cut leaves float partials, which a second kernel
+//            merges; an item inside one share is written directly.  A decode step of any
+//            mix of lengths then keeps every SM streaming until the end.
+//
+// Roles (384 threads, three warpgroups):
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1 (QT = 1: warps 4-7 idle)
+//   warp 8          producer: Q, K and V tiles by TMA; pages one box each, a lane to a page
+//   warp 9          MMA issuer (one thread)
+//   warp 10         scheduler: finds the CTA's next item while the current one runs
+//   warp 11         zeroes V rows that belong to no visible key (a sequence that ends
+//                   inside a tile), so that nothing there, NaN included, reaches P V
+// The CTA runs its items as one stream: the rings of Q, K and V tiles and every barrier's
+// phase go on across items, the first scores of the next item are issued right behind
+// the last P V of this one, and its epilogue overlaps them.
+#pragma once
+
+#include <cstdint>
+
+#include "fa2_paged.cuh"
+#include "ptx.cuh"
+
+namespace fa2 {
+
+struct SeqParams {
+  uint16_t* O;
+  long long o_row, o_head;  // strides in elements
+  float* LSE;               // [H][T]
+  const int* cu;            // [B + 1]
+  const int* seq_lens;      // paged: [B]
+  const int* block_table;   // paged: [B][max_blocks]; nullptr: packed keys
+  float* O_part;            // [2 grid][QT * 128][D]
+  float* LSE_part;          // [2 grid][QT * 128]
+  unsigned int* status;
+  unsigned long long wait_ns;
+  int B, T, Hkv, G, d, tpt;  // tpt: tokens to a tile, 128 / G
+  int causal, window, fault, head_group;
+  int num_blocks, block_size, max_blocks;
+  int box_rows;  // paged: rows of a box, min(block_size, 128)
+  float scale_log2;
+};
+
+template <int D_, int QT_>
+struct SeqCfg {
+  static constexpr int D = D_, QT = QT_;
+  static_assert(QT == 1 || D <= 128, "two accumulators fit tensor memory up to D = 128");
+  static constexpr int KCH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = 128 * D * 2;
+  // Ring stages within 227 KB (tiles of 16, 32, 48, 64 KB).  Two query tiles have a third
+  // slot at D = 128, so that the next item's first tile loads during this one.
+  static constexpr int QS = D == 64 ? 4 : (D == 128 ? (QT == 2 ? 3 : 2) : 1);
+  static constexpr int KS = D == 64 ? 4 : (D == 256 ? 1 : 2);
+  static constexpr int VS = D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1);
+  static constexpr int SMEM = (QS + KS + VS) * TILE + 1024;
+  static_assert(SMEM <= 226 * 1024, "shared memory");
+  static constexpr int THREADS = 384;
+  static constexpr int LAUNCH_REGS = 168;
+  static constexpr int SOFT_REGS = 216, OTHER_REGS = 72;
+  static_assert(2 * 128 * SOFT_REGS + 128 * OTHER_REGS <= THREADS * LAUNCH_REGS, "register re-split");
+  __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256u + t * D; }
+  // D = 64 with two tiles: P in columns of its own (the next scores overwrite S early).
+  static constexpr bool SEP = D == 64 && QT == 2;
+  __host__ __device__ static constexpr uint32_t P_COL(int t) { return 384u + 64u * t; }
+};
+
+enum SeqSite : uint32_t {
+  kQSiteItem = 80, kQSiteItemEmpty, kQSiteProd, kQSiteMmaQ, kQSiteMmaK, kQSiteMmaV, kQSiteMmaP, kQSiteMmaO,
+  kQSiteMmaDrain, kQSiteSoftS, kQSiteSoftO, kQSiteFix, kQSiteClc, kQSiteDrain
+};
+
+constexpr int kSeqItems = 4;  // ring of items handed to the roles
+
+struct SeqItem {
+  int row0, n_tok;   // first packed query row, tokens
+  int kvh;           // key/value head
+  int key0;          // packed: row of the sequence's first key; paged: the request
+  int nk, first;     // keys of the sequence; first one that any row of the item sees
+  int pos;           // position of the item's first token among the keys
+  int lo[2], hi[2];  // key tiles of each query tile
+  int j0, n;         // key tiles of the item: j0 .. j0 + n - 1
+  int part;          // partial slot, -1: O and LSE are written
+  int valid;
+  int pad;
+};
+
+// ------------------------------------------------------------------------------------
+// items
+// ------------------------------------------------------------------------------------
+
+struct SeqLen {
+  int row0, n, nk;
+};
+
+__device__ __forceinline__ SeqLen seq_len(const SeqParams& p, int b) {
+  SeqLen s;
+  s.row0 = min(max(p.cu[b], 0), p.T);
+  s.n = min(max(p.cu[b + 1], s.row0), p.T) - s.row0;
+  s.nk = s.n;
+  if (p.block_table) s.nk = min(max(p.seq_lens[b], 0), p.max_blocks * p.block_size);
+  return s;
+}
+
+// Key tiles that tokens [a, e) of a sequence need; the same for the whole item.
+__device__ __forceinline__ void key_range(const SeqParams& p, const SeqLen& s, int a, int e, int& lo, int& hi) {
+  const int pos = s.nk - s.n;  // of token 0
+  lo = hi = 0;
+  if (a >= e) return;
+  const int last = p.causal ? min(pos + e - 1, s.nk - 1) : s.nk - 1;
+  hi = last >= 0 ? (last >> 7) + 1 : 0;
+  if (p.window > 0) lo = max(0, pos + a - p.window + 1) >> 7;
+  if (hi <= lo) lo = hi = 0;
+}
+
+template <int QT>
+__device__ __forceinline__ void make_item(const SeqParams& p, const SeqLen& s, int b, int kvh, int blk, SeqItem& it) {
+  const int a = blk * (QT * p.tpt), e = min(s.n, a + QT * p.tpt), m = min(e, a + p.tpt);
+  it.row0 = s.row0 + a;
+  it.n_tok = e - a;
+  it.kvh = kvh;
+  it.key0 = p.block_table ? b : s.row0;
+  it.nk = s.nk;
+  it.pos = s.nk - s.n + a;
+  it.first = p.window > 0 ? max(0, it.pos - p.window + 1) : 0;
+  key_range(p, s, a, m, it.lo[0], it.hi[0]);
+  it.lo[1] = it.hi[1] = 0;
+  if (QT == 2) key_range(p, s, m, e, it.lo[1], it.hi[1]);
+  const bool h0 = it.hi[0] > 0, h1 = it.hi[1] > 0;
+  it.j0 = h0 ? (h1 ? min(it.lo[0], it.lo[1]) : it.lo[0]) : it.lo[1];
+  it.n = max(it.hi[0], it.hi[1]) - it.j0;
+  it.part = -1;
+  it.valid = 1;
+}
+
+// The item cut to the key tiles [a, e) counted from its first one.
+__device__ __forceinline__ void cut_item(SeqItem& it, int a, int e) {
+  const int s = it.j0 + a, f = it.j0 + e;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.lo[t] = max(it.lo[t], s);
+    it.hi[t] = min(it.hi[t], f);
+    if (it.hi[t] <= it.lo[t]) it.lo[t] = it.hi[t] = 0;
+  }
+  const bool h0 = it.hi[0] > 0, h1 = it.hi[1] > 0;
+  it.j0 = h0 ? (h1 ? min(it.lo[0], it.lo[1]) : it.lo[0]) : it.lo[1];
+  it.n = max(it.hi[0], it.hi[1]) - it.j0;
+}
+
+// Units of work of block blk of a sequence: its key tiles, at least one.
+template <int QT>
+__device__ __forceinline__ int block_units(const SeqParams& p, const SeqLen& s, int blk) {
+  const int R = QT * p.tpt, a = blk * R, e = min(s.n, a + R), m = min(e, a + p.tpt);
+  int l0, h0, l1 = 0, h1 = 0;
+  key_range(p, s, a, m, l0, h0);
+  if (QT == 2) key_range(p, s, m, e, l1, h1);
+  const int lo = h0 > 0 ? (h1 > 0 ? min(l0, l1) : l0) : l1;
+  return max(1, max(h0, h1) - lo);
+}
+
+// Units of one key/value head of the sequences b0 + lane (0 past B): lanes with few
+// blocks sum their own, the others' are summed by the whole warp.
+template <int QT>
+__device__ __forceinline__ int chunk_units(const SeqParams& p, int b0, int lane) {
+  const int b = b0 + lane;
+  SeqLen s{0, 0, 0};
+  if (b < p.B) s = seq_len(p, b);
+  const int R = QT * p.tpt, nb = (s.n + R - 1) / R;
+  int u = 0;
+  if (nb <= 4)
+    for (int i = 0; i < nb; ++i) u += block_units<QT>(p, s, i);
+  unsigned int many = __ballot_sync(0xffffffffu, nb > 4);
+  while (many) {
+    const int l = __ffs(many) - 1;
+    many &= many - 1;
+    SeqLen o;
+    o.row0 = 0;
+    o.n = __shfl_sync(0xffffffffu, s.n, l);
+    o.nk = __shfl_sync(0xffffffffu, s.nk, l);
+    int part = 0;
+    for (int i = lane; i < (o.n + R - 1) / R; i += 32) part += block_units<QT>(p, o, i);
+    part = __reduce_add_sync(0xffffffffu, part);
+    if (lane == l) u = part;
+  }
+  return u;
+}
+
+__device__ __forceinline__ int warp_inclusive(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Total units of all heads (whole warp; every lane gets the sum).
+template <int QT>
+__device__ __forceinline__ long long total_units(const SeqParams& p, int lane) {
+  long long w = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) w += __reduce_add_sync(0xffffffffu, chunk_units<QT>(p, b0, lane));
+  return w * p.Hkv;
+}
+
+// CTAs that get a share: at least kMinUnits units each.
+constexpr int kMinUnits = 2;
+__device__ __forceinline__ int share_ctas(long long units, int grid) {
+  const long long c = (units + kMinUnits - 1) / kMinUnits;
+  return static_cast<int>(c < grid ? (c > 0 ? c : 1) : grid);
+}
+__device__ __forceinline__ long long share_start(long long units, int ctas, int c) { return units * c / ctas; }
+
+// Where unit x of the linear order (sequence, head, block, key tile) lies.  Whole warp.
+struct UnitAt {
+  int b, kvh, blk, at;  // at: units of the block before x
+  int units;            // of one head of the sequence
+  SeqLen s;
+};
+template <int QT>
+__device__ __forceinline__ UnitAt find_unit(const SeqParams& p, long long x, int lane) {
+  UnitAt r{};
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int u = chunk_units<QT>(p, b0, lane);
+    const int inc = warp_inclusive(u, lane);
+    const long long end = static_cast<long long>(inc) * p.Hkv;
+    const unsigned int m = __ballot_sync(0xffffffffu, end > x);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      r.b = b0 + l;
+      r.units = __shfl_sync(0xffffffffu, u, l);
+      x -= __shfl_sync(0xffffffffu, end, l) - static_cast<long long>(r.units) * p.Hkv;
+      break;
+    }
+    x -= __shfl_sync(0xffffffffu, end, 31);
+  }
+  r.s = seq_len(p, r.b);
+  r.kvh = static_cast<int>(x / r.units);
+  int rem = static_cast<int>(x - static_cast<long long>(r.kvh) * r.units);
+  const int R = QT * p.tpt, nb = (r.s.n + R - 1) / R;
+  for (int i0 = 0; i0 < nb; i0 += 32) {
+    const int u = i0 + lane < nb ? block_units<QT>(p, r.s, i0 + lane) : 0;
+    const int inc = warp_inclusive(u, lane);
+    const unsigned int m = __ballot_sync(0xffffffffu, inc > rem);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      r.blk = i0 + l;
+      rem -= __shfl_sync(0xffffffffu, inc - u, l);
+      break;
+    }
+    rem -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  r.at = rem;
+  return r;
+}
+
+// Packed: blocks with index > level over the sequences, sum_b max(0, nblk_b - level).
+template <int QT>
+__device__ __forceinline__ int blocks_from(const SeqParams& p, int level, int lane) {
+  const int R = QT * p.tpt;
+  int c = 0;
+  for (int b = lane; b < p.B; b += 32) c += max(0, (seq_len(p, b).n + R - 1) / R - level);
+  return __reduce_add_sync(0xffffffffu, c);
+}
+
+// Packed: item w of the order -- head group by head group, in a group the blocks of the
+// highest index (the most keys, when causal) of all sequences first, heads innermost.
+// False when there are fewer items.  Whole warp.
+template <int QT>
+__device__ __forceinline__ bool find_item(const SeqParams& p, int w, int n_blocks, int max_blk, int lane,
+                                          SeqItem& it) {
+  if (w >= n_blocks * p.Hkv) return false;
+  const int per = p.head_group * n_blocks, grp = w / per, at = w - grp * per;
+  const int heads = min(p.head_group, p.Hkv - grp * p.head_group);
+  const int rank = at / heads, kvh = grp * p.head_group + at % heads;
+  int lo = 0, hi = max_blk;  // the largest level with blocks_from(level) > rank
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (blocks_from<QT>(p, mid, lane) > rank) lo = mid; else hi = mid;
+  }
+  int i = rank - blocks_from<QT>(p, lo + 1, lane);  // the i-th sequence with more than lo blocks
+  const int R = QT * p.tpt;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const bool has = b < p.B && (seq_len(p, b).n + R - 1) / R > lo;
+    const unsigned int m = __ballot_sync(0xffffffffu, has);
+    const int c = __popc(m);
+    if (i < c) {
+      const bool mine = has && __popc(m & ((1u << lane) - 1u)) == i;
+      const int l = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      make_item<QT>(p, seq_len(p, b0 + l), b0 + l, kvh, lo, it);
+      return true;
+    }
+    i -= c;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------------------------
+// cluster launch control: the index of a CTA of this grid that has not started
+// ------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void clc_try_cancel(uint4* response, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(response)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The cancelled CTA's blockIdx.x, or -1 when none was left.
+__device__ __forceinline__ int clc_index(const uint4* response) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
+}
+
+// 4-D tiled load (a page's rows of one head).
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// ------------------------------------------------------------------------------------
+// the kernel
+// ------------------------------------------------------------------------------------
+
+// Keys of tile j that some row of the item sees, counted from the tile's first key.
+__device__ __forceinline__ void tile_keys(const SeqItem& it, int j, int& a, int& e) {
+  a = max(it.first - j * 128, 0);
+  e = min(it.nk - j * 128, 128);
+}
+
+template <int D, bool BF16, int QT>
+__global__ void __launch_bounds__(384, 1)
+fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const SeqParams p) {
+  using C = SeqCfg<D, QT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + C::QS * C::TILE;
+  uint8_t* sV = sK + C::KS * C::TILE;
+
+  __shared__ __align__(16) uint4 clc_response;
+  constexpr int NI = kSeqItems;
+  __shared__ __align__(16) SeqItem items[NI];
+  __shared__ uint64_t item_full[NI], item_empty[NI], clc_full;
+  __shared__ uint64_t q_full[C::QS], q_empty[C::QS], k_full[C::KS], k_empty[C::KS];
+  __shared__ uint64_t v_full[C::VS], v_empty[C::VS], v_raw[C::VS];
+  __shared__ uint64_t s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  griddep_launch_dependents();  // the merge kernel waits for this grid before it reads
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const bool paged = p.block_table != nullptr;
+  WaitCtl wc{p.status, &abort_flag, p.wait_ns};
+
+  if (threadIdx.x == 8 * 32) {
+    abort_flag = 0;
+    for (int i = 0; i < NI; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], 3 + 4 * QT);  // producer, MMA, V fix and the softmax warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    mbar_init(&clc_full, 1);
+    for (int i = 0; i < C::QS; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
+    for (int i = 0; i < C::KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < C::VS; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_raw[i], 1);
+    }
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = tmem_slot;
+
+  if (warp >= 8) {
+    regs_dec<C::OTHER_REGS>();
+    if (warp == 10) {
+      // ---------------------------------------------------------------- scheduler
+      int ii = 0;
+      auto publish = [&](const SeqItem& it) -> bool {
+        const int s = ii % NI;
+        bool ok = true;
+        if (ii >= NI) ok = mbar_wait(&item_empty[s], ((ii / NI) - 1) & 1, wc, kQSiteItemEmpty);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (lane == 0) {
+          items[s] = it;
+          mbar_arrive(&item_full[s]);
+        }
+        ++ii;
+        return true;
+      };
+      SeqItem it{};
+      bool ok = true;
+      if (paged) {
+        const long long units = total_units<QT>(p, lane);
+        const int ctas = share_ctas(units, gridDim.x), c = blockIdx.x;
+        long long x = share_start(units, ctas, c);
+        const long long xe = c < ctas ? share_start(units, ctas, c + 1) : x;
+        if (x < xe) {
+          UnitAt u = find_unit<QT>(p, x, lane);
+          const int R = QT * p.tpt;
+          while (ok) {
+            const int len = block_units<QT>(p, u.s, u.blk);
+            const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
+            make_item<QT>(p, u.s, u.b, u.kvh, u.blk, it);
+            if (u.at > 0 || take < len) {
+              cut_item(it, u.at, u.at + take);
+              it.part = 2 * c + (u.at > 0 ? 0 : 1);
+            }
+            ok = publish(it);
+            x += take;
+            if (x >= xe) break;
+            u.at = 0;
+            if (++u.blk >= (u.s.n + R - 1) / R) {
+              u.blk = 0;
+              if (++u.kvh >= p.Hkv) {
+                u.kvh = 0;
+                do u.s = seq_len(p, ++u.b); while (u.s.n == 0 && u.b + 1 < p.B);  // units are left
+              }
+            }
+          }
+        }
+      } else {
+        int mb = 0;
+        for (int b = lane; b < p.B; b += 32) mb = max(mb, (seq_len(p, b).n + QT * p.tpt - 1) / (QT * p.tpt));
+        const int max_blk = __reduce_max_sync(0xffffffffu, mb), n_blocks = blocks_from<QT>(p, 0, lane);
+        int w = blockIdx.x;
+        for (int k = 0; ok && w >= 0; ++k) {
+          if (find_item<QT>(p, w, n_blocks, max_blk, lane, it)) ok = publish(it);
+          // The next index only once the item before this one is done with: a CTA holds
+          // at most one item that it has not begun.
+          if (ok && ii >= 2)
+            ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[(ii - 2) % NI], ((ii - 2) / NI) & 1, wc, kQSiteItemEmpty));
+          if (!ok) break;
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the response was read before it is written again
+            mbar_arrive_expect_tx(&clc_full, 16);
+            clc_try_cancel(&clc_response, &clc_full);
+          }
+          __syncwarp();
+          volatile int no_abort = 0;  // the response always lands before the CTA leaves
+          WaitCtl cw{p.status, &no_abort, p.wait_ns};
+          ok = __all_sync(0xffffffffu, mbar_wait(&clc_full, k & 1, cw, kQSiteClc));
+          if (!ok) break;
+          w = lane == 0 ? clc_index(&clc_response) : 0;
+          w = __shfl_sync(0xffffffffu, w, 0);
+        }
+      }
+      it.valid = 0;
+      if (ok) publish(it);
+    } else if (warp == 8) {
+      // ---------------------------------------------------------------- producer
+      const uint64_t keep = policy_evict_last();
+      int qc = 0, kc = 0, vc = 0;       // tiles loaded
+      unsigned int raw = 0;             // V slots whose last load went to v_raw
+      unsigned int raw_par = 0;         // parity of the loads on v_raw, per slot
+      bool ok = true, skipped = false;  // test hook: the first K tile was not loaded
+      const int nbox = 128 / (paged ? p.box_rows : 128);
+      auto wait_all = [&](uint64_t* bar, uint32_t par) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, par, wc, kQSiteProd)) != 0;
+      };
+      auto load_q = [&](const SeqItem& it, int t) -> bool {
+        const int s = qc % C::QS;
+        if (qc >= C::QS && !wait_all(&q_empty[s], ((qc / C::QS) - 1) & 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[s], C::KCH * 128 * p.G * p.tpt);
+          for (int c = 0; c < C::KCH; ++c)
+            tma_load_3d(sQ + s * C::TILE + c * C::CHUNK, &tmQ, &q_full[s], c * 64, it.kvh * p.G,
+                        it.row0 + t * p.tpt);
+        }
+        ++qc;
+        return true;
+      };
+      // Lane i: the page of box i of tile j (read ahead of the tile's loads).
+      auto pages_of = [&](const SeqItem& it, int j) -> int {
+        int a, e, pg = 0;
+        tile_keys(it, j, a, e);
+        if (lane < nbox && lane * p.box_rows < e && (lane + 1) * p.box_rows > a) {
+          pg = p.block_table[static_cast<size_t>(it.key0) * p.max_blocks + (j * 128 + lane * p.box_rows) / p.block_size];
+          if (pg < 0 || pg >= p.num_blocks) {
+            atomicCAS(p.status, 0u, kStatusInvalid | (kPSiteBlock << 8));
+            pg = p.num_blocks;  // outside the map: reads as zeros
+          }
+        }
+        return pg;
+      };
+      auto load_tile = [&](const SeqItem& it, int j, int pg, const CUtensorMap* map, uint8_t* dst, uint64_t* bar) {
+        if (!paged) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, C::TILE);
+            for (int c = 0; c < C::KCH; ++c)
+              tma_load_3d_hint(dst + c * C::CHUNK, map, bar, c * 64, it.key0 + j * 128, it.kvh, keep);
+          }
+          return;
+        }
+        int a, e;
+        tile_keys(it, j, a, e);
+        const int i0 = a / p.box_rows, n = (e + p.box_rows - 1) / p.box_rows - i0;
+        if (lane == 0) mbar_arrive_expect_tx(bar, n * p.box_rows * 128 * C::KCH);
+        __syncwarp();
+        for (int x0 = 0; x0 < n * C::KCH; x0 += 32) {
+          const int x = x0 + lane, i = i0 + x / C::KCH, c = x % C::KCH;
+          const int page = __shfl_sync(0xffffffffu, pg, i & 31);
+          if (x < n * C::KCH)
+            tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64,
+                        (j * 128 + i * p.box_rows) % p.block_size, it.kvh, page);
+        }
+      };
+      auto load_k = [&](const SeqItem& it, int j, int pg) -> bool {
+        const int s = kc % C::KS;
+        if (kc >= C::KS && !wait_all(&k_empty[s], ((kc / C::KS) - 1) & 1)) return false;
+        if (p.fault == 1 && kc == 0) skipped = true;
+        else load_tile(it, j, pg, &tmK, sK + s * C::TILE, &k_full[s]);
+        ++kc;
+        return true;
+      };
+      auto load_v = [&](const SeqItem& it, int j, int pg) -> bool {
+        const int s = vc % C::VS;
+        if (vc >= C::VS && !wait_all(&v_empty[s], ((vc / C::VS) - 1) & 1)) return false;
+        int a, e;
+        tile_keys(it, j, a, e);
+        const bool fix = a > 0 || e < 128;
+        load_tile(it, j, pg, &tmV, sV + s * C::TILE, fix ? &v_raw[s] : &v_full[s]);
+        raw = fix ? raw | (1u << s) : raw & ~(1u << s);
+        if (fix) raw_par ^= 1u << s;
+        ++vc;
+        return true;
+      };
+      SeqItem old{};  // QT = 1: the tile whose V is still to be loaded, behind the next K
+      int old_j = -1, old_pg = 0;
+      for (int ii = 0; ok; ++ii) {
+        if (!(ok = wait_all(&item_full[ii % NI], (ii / NI) & 1))) break;
+        const SeqItem it = items[ii % NI];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[ii % NI]);
+        if (!it.valid) break;
+        if (it.n == 0) continue;
+        int pg = paged ? pages_of(it, it.j0) : 0;
+        if (it.hi[0] > 0) ok = load_q(it, 0);
+        for (int jj = 0; jj < it.n && ok; ++jj) {
+          const int j = it.j0 + jj;
+          const int pg_next = paged && jj + 1 < it.n ? pages_of(it, j + 1) : 0;
+          ok = load_k(it, j, pg);
+          if (QT == 2) {
+            if (ok && jj == 0 && it.hi[1] > 0) ok = load_q(it, 1);
+            ok = ok && load_v(it, j, pg);
+          } else {
+            if (ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
+            old = it;
+            old_j = j;
+            old_pg = pg;
+          }
+          pg = pg_next;
+        }
+      }
+      if (QT == 1 && ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
+      if (lane == 0) {
+        // Every copy that was issued lands before the CTA leaves, on a timeout too.
+        volatile int no_abort = 0;
+        WaitCtl dw{p.status, &no_abort, 100000000ull};
+        for (int i = max(0, qc - C::QS); i < qc; ++i) mbar_wait(&q_full[i % C::QS], (i / C::QS) & 1, dw, kQSiteDrain);
+        for (int i = max(0, kc - C::KS); i < kc; ++i)
+          if (!(skipped && i == 0)) mbar_wait(&k_full[i % C::KS], (i / C::KS) & 1, dw, kQSiteDrain);
+        for (int i = max(0, vc - C::VS); i < vc; ++i) {
+          const int s = i % C::VS;
+          if (raw >> s & 1) mbar_wait(&v_raw[s], (raw_par >> s & 1) ^ 1, dw, kQSiteDrain);
+          else mbar_wait(&v_full[s], (i / C::VS) & 1, dw, kQSiteDrain);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 11) {
+      // ---------------------------------------------------------------- V rows of no visible key
+      int vc = 0;
+      unsigned int par = 0;
+      bool ok = true;
+      for (int ii = 0; ok; ++ii) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem));
+        if (!ok) break;
+        const SeqItem it = items[ii % NI];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[ii % NI]);
+        if (!it.valid) break;
+        for (int jj = 0; jj < it.n && ok; ++jj, ++vc) {
+          int a, e;
+          tile_keys(it, it.j0 + jj, a, e);
+          if (a <= 0 && e >= 128) continue;
+          const int s = vc % C::VS;
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_raw[s], par >> s & 1, wc, kQSiteFix));
+          if (!ok) break;
+          par ^= 1u << s;
+          uint8_t* v = sV + s * C::TILE + (lane & 7) * 16;
+          for (int r = lane >> 3; r < 128; r += 4)
+            if (r < a || r >= e)
+              for (int c = 0; c < C::KCH; ++c)
+                *reinterpret_cast<uint4*>(v + c * C::CHUNK + r * 128) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[s]);
+        }
+      }
+      __syncwarp();
+    } else if (lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer (warp 9)
+      constexpr uint32_t id_qk = idesc_f16(128, 128, BF16, false, false);
+      constexpr uint32_t id_pv = idesc_f16(128, D, BF16, false, true);
+      const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+      int ii = 0, qc = 0, kc = 0, vc = 0;
+      int sc[2] = {0, 0};   // score products issued per tile
+      int ic[2] = {0, 0};   // items begun per tile
+      struct Cur {
+        int lo[2], hi[2], qs[2], j0, n;
+      };
+      // The next item with key tiles: 1, or 0 at the end and -1 on a timeout.
+      auto fetch = [&](Cur& c) -> int {
+        for (;; ) {
+          const int s = ii % NI;
+          if (!mbar_wait(&item_full[s], (ii / NI) & 1, wc, kQSiteItem)) return -1;
+          const SeqItem& it = items[s];
+          const bool valid = it.valid != 0;
+          c.lo[0] = it.lo[0], c.lo[1] = it.lo[1], c.hi[0] = it.hi[0], c.hi[1] = it.hi[1];
+          c.j0 = it.j0, c.n = it.n;
+          mbar_arrive(&item_empty[s]);
+          ++ii;
+          if (!valid) return 0;
+          if (c.n == 0) continue;
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+            if (c.hi[t] > 0) c.qs[t] = qc++;
+          return 1;
+        }
+      };
+      // S of tile t (Q load number q) against K slot ks.
+      auto issue_s = [&](int t, int q, int ks, bool last) {
+        const int b = QT == 2 ? t : (sc[0] & 1);
+        const uint32_t dt = tbase + b * 128, qa = aQ + (q % C::QS) * C::TILE, ka = aK + ks * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+          umma_ss(dt, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_qk, kk > 0);
+        }
+        umma_commit(&s_full[b]);
+        if (last) umma_commit(&q_empty[q % C::QS]);
+        ++sc[t];
+      };
+      auto issue_pv = [&](int t, uint32_t a_col, int vs, bool acc) {
+        const uint32_t va = aV + vs * C::TILE, dt = tbase + C::O_COL(t);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ts(dt, tbase + a_col + kk * 8, sdesc_sw128(va + kk * 2048, C::CHUNK, 1024), id_pv,
+                  (acc || kk > 0) ? 1u : 0u);
+        umma_commit(&o_done[t]);
+        umma_commit(&v_empty[vs]);
+      };
+      Cur cur{}, nxt{};
+      int have = fetch(cur);
+      bool ok = have >= 0;
+      // First scores of an item's tile t; k_ok: K has been waited for.
+      auto first_s = [&](const Cur& c, int t, bool& k_ok) -> bool {
+        if (c.hi[t] == 0 || c.lo[t] != c.j0) return true;
+        const int q = c.qs[t];
+        if (!mbar_wait(&q_full[q % C::QS], (q / C::QS) & 1, wc, kQSiteMmaQ)) return false;
+        if (!k_ok && !mbar_wait(&k_full[kc % C::KS], (kc / C::KS) & 1, wc, kQSiteMmaK)) return false;
+        k_ok = true;
+        if (C::SEP && sc[t] > 0 && !mbar_wait(&s_free[t], (sc[t] - 1) & 1, wc, kQSiteMmaP)) return false;
+        tc_fence_after();
+        issue_s(t, q, kc % C::KS, c.hi[t] == c.j0 + 1);
+        return true;
+      };
+      if (have == 1) {
+        bool k_ok = false;
+        for (int t = 0; t < QT && ok; ++t) ok = first_s(cur, t, k_ok);
+        if (ok) {
+          umma_commit(&k_empty[kc % C::KS]);
+          ++kc;
+        }
+      }
+      while (ok && have == 1) {
+        int more = 1;
+        for (int jj = 0; jj < cur.n && ok; ++jj, ++vc) {
+          const int j = cur.j0 + jj, vs = vc % C::VS;
+          const bool last = jj + 1 == cur.n;
+          bool k_ok = false, v_ok = false, fetched = false;
+          // S of the step after this one: this item's next key tile or the next item's first.
+          auto next_s = [&](int t) -> bool {
+            if (last) {
+              if (!fetched) {
+                more = fetch(nxt);
+                fetched = true;
+                if (more < 0) return false;
+              }
+              return more != 1 || first_s(nxt, t, k_ok);
+            }
+            if (j + 1 < cur.lo[t] || j + 1 >= cur.hi[t]) return true;
+            if (!k_ok && !mbar_wait(&k_full[kc % C::KS], (kc / C::KS) & 1, wc, kQSiteMmaK)) return false;
+            k_ok = true;
+            const int q = cur.qs[t];
+            if (j + 1 == cur.lo[t] && !mbar_wait(&q_full[q % C::QS], (q / C::QS) & 1, wc, kQSiteMmaQ)) return false;
+            if (C::SEP && sc[t] > 0 && !mbar_wait(&s_free[t], (sc[t] - 1) & 1, wc, kQSiteMmaP)) return false;
+            tc_fence_after();
+            issue_s(t, q, kc % C::KS, j + 2 == cur.hi[t]);
+            return true;
+          };
+          // O_t += P_t V.  pc: number of the product (its P is phase pc).
+          auto pv = [&](int t) -> bool {
+            if (j < cur.lo[t] || j >= cur.hi[t]) return true;
+            const bool first = j == cur.lo[t];
+            if (!v_ok && !mbar_wait(&v_full[vs], (vc / C::VS) & 1, wc, kQSiteMmaV)) return false;
+            v_ok = true;
+            if (first) {
+              // The item before has read its output out of the accumulator.
+              if (ic[t] > 0 && !mbar_wait(&o_free[t], (ic[t] - 1) & 1, wc, kQSiteMmaO)) return false;
+              ++ic[t];
+            }
+            return true;
+          };
+          if constexpr (QT == 1) {
+            // S of the next step goes ahead of this step's P: two S blocks in turn.
+            const int pc = sc[0] - 1;
+            ok = next_s(0);
+            if (!ok) break;
+            if (!last || more == 1) {
+              umma_commit(&k_empty[kc % C::KS]);
+              ++kc;
+            }
+            ok = pv(0) && mbar_wait(&p_ready[pc & 1], (pc >> 1) & 1, wc, kQSiteMmaP);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(0, (pc & 1) * 128, vs, j > cur.lo[0]);
+          } else {
+            auto do_pv = [&](int t, int pc) -> bool {
+              if (!pv(t)) return false;
+              if (j < cur.lo[t] || j >= cur.hi[t]) return true;
+              if (!mbar_wait(&p_ready[t], pc & 1, wc, kQSiteMmaP)) return false;
+              tc_fence_after();
+              const uint32_t va = aV + vs * C::TILE, dt = tbase + C::O_COL(t);
+              const uint32_t a_col = C::SEP ? C::P_COL(t) : t * 128u;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_ts(dt, tbase + a_col + kk * 8, sdesc_sw128(va + kk * 2048, C::CHUNK, 1024), id_pv,
+                        (j > cur.lo[t] || kk > 0) ? 1u : 0u);
+              umma_commit(&o_done[t]);
+              return true;
+            };
+            const int p0 = sc[0] - 1, p1 = sc[1] - 1;
+            if constexpr (C::SEP) ok = next_s(0) && next_s(1) && do_pv(0, p0) && do_pv(1, p1);
+            else ok = do_pv(0, p0) && next_s(0) && do_pv(1, p1) && next_s(1);
+            // A slot is only released once its load has landed.
+            if (ok && !v_ok) ok = mbar_wait(&v_full[vs], (vc / C::VS) & 1, wc, kQSiteMmaV);
+            const bool adv = !last || more == 1;
+            if (ok && adv && !k_ok) ok = mbar_wait(&k_full[kc % C::KS], (kc / C::KS) & 1, wc, kQSiteMmaK);
+            if (!ok) break;
+            umma_commit(&v_empty[vs]);
+            if (adv) {
+              umma_commit(&k_empty[kc % C::KS]);
+              ++kc;
+            }
+          }
+        }
+        have = ok ? more : -1;
+        cur = nxt;
+      }
+      // Every product issued completes before tensor memory is released.
+      umma_commit(&drain);
+      volatile int no_abort = 0;
+      WaitCtl dw{p.status, &no_abort, p.wait_ns};
+      mbar_wait(&drain, 0, dw, kQSiteMmaDrain);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ softmax
+    regs_inc<C::SOFT_REGS>();
+    const int t = warp >> 2, wq = warp & 3;
+    const int r_loc = wq * 32 + lane;
+    const int G = p.G, tpt = p.tpt;
+    const int tok_r = r_loc / G, g_r = r_loc - tok_r * G;
+    const uint32_t o_col = C::O_COL(t);
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32);
+    const float sl2 = p.scale_log2;
+    int sc = 0;  // steps of this tile so far
+    bool ok = t < QT;
+    for (int ii = 0; ok; ++ii) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem));
+      if (!ok) break;
+      const SeqItem& it = items[ii % NI];  // held until the item is done
+      if (!it.valid) break;
+      const int lo = t ? it.lo[1] : it.lo[0], steps = (t ? it.hi[1] : it.hi[0]) - lo;
+      const int tok = t * tpt + tok_r;
+      const bool row_ok = tok_r < tpt && tok < it.n_tok;
+      const bool live = __any_sync(0xffffffffu, row_ok);
+      const int pos = it.pos + tok;
+      const int klast = p.causal ? min(pos, it.nk - 1) : it.nk - 1;
+      const int kfirst = p.window > 0 ? pos - p.window + 1 : 0;
+      float m = -INFINITY;  // running maximum, log2 units
+      float l = 0.f;        // sum of the weights: the log-sum-exp
+      float lr = 0.f;       // sum of the weights as rounded for P V: the divisor of O
+      for (int step = 0; step < steps; ++step, ++sc) {
+        // QT = 1: the two S blocks in turn; else one block to a tile.
+        const int buf = QT == 1 ? (sc & 1) : t;
+        const uint32_t par = QT == 1 ? ((sc >> 1) & 1) : (sc & 1);
+        const uint32_t s_col = buf * 128u;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[buf], par, wc, kQSiteSoftS));
+        if (!ok) break;
+        if (live) {
+          tc_fence_after();
+          uint32_t sr[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32(tmem_addr(tbase, lane_base, s_col + 32 * c), *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+          tmem_wait_ld();
+          reg_fence(sr);
+          if (C::SEP) {  // the S block may take the next scores
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[t]);
+          }
+          // Keys past the row's last one or before its window.
+          const int kc0 = (lo + step) * 128;
+          const int hi_lim = klast - kc0 + 1, lo_lim = kfirst - kc0;
+          if (__any_sync(0xffffffffu, hi_lim < 128 || lo_lim > 0)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= hi_lim || i < lo_lim) sr[i] = __float_as_uint(-INFINITY);
+          }
+          float mx[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx[k] = fmax3(__uint_as_float(sr[k]), __uint_as_float(sr[k + 8]), __uint_as_float(sr[k + 16]));
+#pragma unroll
+          for (int i = 24; i < 120; i += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mx[k] = fmax3(mx[k], __uint_as_float(sr[i + k]), __uint_as_float(sr[i + k + 8]));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(sr[120 + k]));
+          mx[0] = fmax3(mx[0], mx[1], mx[2]);
+          mx[3] = fmax3(mx[3], mx[4], mx[5]);
+          mx[6] = fmaxf(mx[6], mx[7]);
+          mx[0] = fmax3(mx[0], mx[3], mx[6]);
+          const float m_new = fmaxf(m, mx[0] * sl2);
+          if (step == 0) {
+            m = m_new;
+          } else {
+            // The stale maximum is kept until it is more than 2^8 behind.
+            const bool need = m_new - m > 8.0f;
+            if (__any_sync(0xffffffffu, need)) {
+              const float f = need ? ex2_approx(m - m_new) : 1.0f;
+              if (need) m = m_new;
+              l *= f;
+              lr *= f;
+              ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (sc - 1) & 1, wc, kQSiteSoftO));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tmem_addr(tbase, lane_base, o_col + 32 * c), r);
+                tmem_wait_ld();
+                reg_fence(r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                tmem_st32(tmem_addr(tbase, lane_base, o_col + 32 * c), r);
+              }
+            }
+          }
+          const uint64_t sl2x2 = f2_pack(sl2, sl2);
+          const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          const uint64_t negm2 = f2_pack(neg_m, neg_m);
+          uint64_t sum2[4] = {0, 0, 0, 0}, sumr2[4] = {0, 0, 0, 0};
+          if (C::SEP && step > 0) {  // the P V product before may still read P
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (sc - 1) & 1, wc, kQSiteSoftO));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const uint32_t p_col = C::SEP ? C::P_COL(t) : s_col;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int k = 64 * h + 2 * i;
+              float a, b;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), sl2x2, negm2), a, b);
+              a = ex2_approx(a);
+              b = ex2_approx(b);
+              sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(a, b));
+              pk[i] = pack2<BF16>(a, b);
+              float r0, r1;
+              unpack2<BF16>(pk[i], r0, r1);
+              sumr2[i & 3] = f2_add(sumr2[i & 3], f2_pack(r0, r1));
+            }
+            tmem_st32(tmem_addr(tbase, lane_base, p_col + 32 * h), pk);
+          }
+          float x0, x1;
+          f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), x0, x1);
+          l += x0 + x1;
+          f2_unpack(f2_add(f2_add(sumr2[0], sumr2[1]), f2_add(sumr2[2], sumr2[3])), x0, x1);
+          lr += x0 + x1;
+          tmem_wait_st();
+          tc_fence_before();
+        } else if (C::SEP) {
+          // A warp without rows keeps the barriers' counts.
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[t]);
+          if (step > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (sc - 1) & 1, wc, kQSiteSoftO));
+            if (!ok) break;
+          }
+        }
+        // QT = 1: S of the item's last step was issued ahead of the P V before it, which may
+        // be pending.  It is waited for before the last P is handed over, so that no later
+        // product can complete meanwhile and the wait below stays within one phase.
+        if (QT == 1 && step == steps - 1 && step >= 1) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (sc - 1) & 1, wc, kQSiteSoftO));
+          if (!ok) break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[buf]);
+      }
+      if (!ok) break;
+      if (steps > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (sc - 1) & 1, wc, kQSiteSoftO));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // A row that sees no key: O = 0, LSE = -inf.
+      const float inv_l = (l > 0.f && lr > 0.f) ? 1.0f / lr : 0.f;
+      const float lse = (l > 0.f) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      const int part = it.part;
+      if (live) {
+        const int row = it.row0 + tok, head = it.kvh * G + g_r;
+        uint16_t* orow = p.O + row * p.o_row + head * p.o_head;
+        const size_t prow = (static_cast<size_t>(max(part, 0)) * QT + t) * 128 + r_loc;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          if (steps > 0) {
+            tmem_ld32(tmem_addr(tbase, lane_base, o_col + 32 * c), r);
+            tmem_wait_ld();
+            reg_fence(r);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+          }
+          if (part < 0) {
+            if (row_ok) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (c * 32 + 8 * i < p.d) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    w[e] = pack2<BF16>(__uint_as_float(r[8 * i + 2 * e]) * inv_l,
+                                       __uint_as_float(r[8 * i + 2 * e + 1]) * inv_l);
+                  *reinterpret_cast<uint4*>(orow + c * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+          } else if (row_ok && l > 0.f) {
+            float4* dst = reinterpret_cast<float4*>(p.O_part + prow * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(r[4 * i]) * inv_l, __uint_as_float(r[4 * i + 1]) * inv_l,
+                                   __uint_as_float(r[4 * i + 2]) * inv_l, __uint_as_float(r[4 * i + 3]) * inv_l);
+          }
+        }
+        if (row_ok) {
+          if (part < 0) p.LSE[static_cast<size_t>(head) * p.T + row] = lse;
+          else p.LSE_part[prow] = lse;
+        }
+      }
+      if (steps > 0) tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (steps > 0) mbar_arrive(&o_free[t]);
+        mbar_arrive(&item_empty[ii % NI]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// merge of the partials
+// ------------------------------------------------------------------------------------
+
+// CTA x looks at the boundary between shares x and x + 1.  If it is the first boundary
+// inside a block of rows, the shares that hold the block are merged, a warp to a row
+// (blockIdx.y: every gridDim.y-th of them):
+//   M = max L_s,  O = sum e^{L_s - M} O_s / sum e^{L_s - M},  LSE = M + ln sum e^{L_s - M}.
+template <int D, bool BF16, int QT>
+__global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p, int grid) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long units = total_units<QT>(p, lane);
+  const int ctas = share_ctas(units, grid), c = blockIdx.x + 1;
+  if (c >= ctas || units == 0) return;
+  const long long x = share_start(units, ctas, c);
+  const UnitAt u = find_unit<QT>(p, x, lane);
+  if (u.at == 0 || share_start(units, ctas, c - 1) > x - u.at) return;
+  const long long end = x - u.at + block_units<QT>(p, u.s, u.blk);
+  int last = c;  // the last share with a part of the block
+  while (last + 1 < ctas && share_start(units, ctas, last + 1) < end) ++last;
+  const int a = u.blk * QT * p.tpt, n_tok = min(u.s.n, a + QT * p.tpt) - a;
+  griddep_wait();
+  constexpr int PER = D / 32;
+  for (int i = blockIdx.y * 8 + warp; i < n_tok * p.G; i += 8 * gridDim.y) {
+    const int tok = i / p.G, g = i - tok * p.G;
+    const int t = tok / p.tpt;
+    const int r = t * 128 + (tok - t * p.tpt) * p.G + g;
+    const auto slot = [&](int s) {  // row of part s (0: the share that holds the block's start)
+      return (static_cast<size_t>(2 * (c - 1 + s) + (s == 0 ? 1 : 0)) * QT) * 128 + r;
+    };
+    const int parts = last - c + 2;
+    float M = -INFINITY;
+    for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.LSE_part[slot(s)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[PER] = {}, wsum = 0.f;
+    if (M != -INFINITY) {
+      for (int s = 0; s < parts; ++s) {
+        const float L = p.LSE_part[slot(s)];
+        if (L == -INFINITY) continue;  // the row sees none of the share's keys
+        const float w = exp2f((L - M) * 1.4426950408889634f);
+        wsum += w;
+        const float* src = p.O_part + slot(s) * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+      }
+    }
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const int row = u.s.row0 + a + tok, head = u.kvh * p.G + g;
+    uint16_t* dst = p.O + row * p.o_row + head * p.o_head + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+      if (lane * PER + e < p.d)
+        *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0)
+      p.LSE[static_cast<size_t>(head) * p.T + row] = wsum > 0.f ? M + logf(wsum) : -INFINITY;
+  }
+}
+
+}  // namespace fa2

@@ -1,5 +1,5 @@
-// Attention over packed sequences with grouped heads, and over paged caches: plain
-// kernels, one warp to a row, right for every size.
+// Backward over packed sequences with grouped heads: plain kernels, one warp to a row,
+// right for every size.
 #pragma once
 
 #include <cstdint>
@@ -13,21 +13,14 @@ struct Packed {
   uint16_t* data;
   long long row, head;
 };
-struct Cache {
-  const uint16_t* data;
-  long long block, head, row;
-};
 
 struct VarlenParams {
   Packed Q, K, V, O, dO, dQ, dK, dV;
-  Cache Kc, Vc;
   float* LSE;  // [H][T]
   float* Dg;   // [H][T]
   const int* cu;
-  const int* seq_lens;
-  const int* block_table;
   unsigned int* status;
-  int B, T, H, Hkv, d, causal, window, num_blocks, block_size, max_blocks;
+  int B, T, H, Hkv, d, causal, window;
   float scale;
 };
 
@@ -72,54 +65,6 @@ __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
-}
-
-// One warp to a (row, query head); lane l holds columns 8 l .. 8 l + 7.
-template <bool BF16, bool PAGED>
-__global__ void __launch_bounds__(128) fa2_varlen_fwd_plain(const VarlenParams p) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, lane = threadIdx.x & 31;
-  if (t >= p.T) return;
-  const int b = seq_of_row(p.cu, p.B, p.T, t);
-  if (b < 0) return;
-  int start, len;
-  seq_rows(p.cu, b, p.T, start, len);
-  const int keys = PAGED ? min(max(p.seq_lens[b], 0), p.max_blocks * p.block_size) : len;
-  const int pos = t - start + keys - len;  // last key of a causal row
-  const int hi = p.causal ? min(pos + 1, keys) : keys;
-  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  const int hk = h / (p.H / p.Hkv);
-  const bool on = lane * 8 < p.d;
-  float q[8] = {}, acc[8] = {};
-  if (on) load8<BF16>(p.Q.data + t * p.Q.row + h * p.Q.head + lane * 8, q);
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const uint16_t *kp, *vp;
-    bool there = true;
-    if constexpr (PAGED) {
-      const int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + j / p.block_size];
-      there = blk >= 0 && blk < p.num_blocks;
-      if (!there && lane == 0) atomicCAS(p.status, 0u, kStatusInvalid | (kPSiteBlock << 8));
-      kp = p.Kc.data + blk * p.Kc.block + hk * p.Kc.head + (j % p.block_size) * p.Kc.row;
-      vp = p.Vc.data + blk * p.Vc.block + hk * p.Vc.head + (j % p.block_size) * p.Vc.row;
-    } else {
-      kp = p.K.data + (start + j) * p.K.row + hk * p.K.head;
-      vp = p.V.data + (start + j) * p.V.row + hk * p.V.head;
-    }
-    float k[8] = {}, v[8] = {};
-    if (on && there) {
-      load8<BF16>(kp + lane * 8, k);
-      load8<BF16>(vp + lane * 8, v);
-    }
-    const float s = dot8(q, k) * p.scale;
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn), e = expf(s - mn);
-    m = mn;
-    l = l * f + e;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = acc[i] * f + e * v[i];
-  }
-  if (on) store8<BF16>(p.O.data + t * p.O.row + h * p.O.head + lane * 8, acc, l > 0.f ? 1.f / l : 0.f);
-  if (lane == 0) p.LSE[static_cast<size_t>(h) * p.T + t] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 // dQ and D of a (row, query head).

@@ -11,8 +11,8 @@
 #include "../../include/fa2.h"
 #include "fa2_host.h"
 #include "fa2_paged.cuh"
+#include "fa2_seq_bwd.cuh"
 #include "fa2_seq_fwd.cuh"
-#include "fa2_varlen.cuh"
 
 namespace {
 
@@ -24,7 +24,7 @@ constexpr int kMaxGroup = 128;  // query heads to a key/value head: rows of one 
 
 int check_sizes(int B, int T, int H, int Hkv, int d, int max_d) {
   if (B < 1 || T < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || H / Hkv > kMaxGroup) return FA2_ERR_INVALID_ARG;
-  if (B > (1 << 24) || T > (1 << 30) || H > (1 << 16)) return FA2_ERR_INVALID_ARG;
+  if (B > (1 << 24) || T > (1 << 30) || H > 65535) return FA2_ERR_INVALID_ARG;
   if (d < 8 || d > max_d || d % 8 != 0) return FA2_ERR_UNSUPPORTED;
   return FA2_OK;
 }
@@ -50,9 +50,6 @@ bool cache_ok(const fa2_cache* x, int blocks, int heads, int rows, int d) {
          (heads <= 1 || stride_ok(x->stride_head, d)) && (rows <= 1 || stride_ok(x->stride_row, d));
 }
 
-fa2::Packed packed(const fa2_packed* x) {
-  return {static_cast<uint16_t*>(x->data), x->stride_row, x->stride_head};
-}
 // ---- forward over packed sequences and paged caches ----
 
 int fwd_tile_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
@@ -164,7 +161,7 @@ fa2::SeqParams seq_params(const fa2_packed* O, float* LSE, const int* cu, unsign
   p.wait_ns = fa2::host_wait_ns();
   p.fault = fa2::host_fault();
   p.B = B, p.T = T, p.Hkv = Hkv, p.G = H / Hkv, p.d = d, p.tpt = 128 / p.G;
-  p.causal = causal, p.window = window;
+  p.causal = causal, p.window = std::min(window, 1 << 30);  // longer than any sequence
   p.scale_log2 = scale * 1.4426950408889634f;
   return p;
 }
@@ -179,6 +176,54 @@ size_t paged_opart_bytes(int grid, int qt, int d) {
 }
 size_t paged_bytes(int grid, int qt, int d) {
   return paged_opart_bytes(grid, qt, d) + static_cast<size_t>(grid) * 2 * qt * 128 * 4;
+}
+
+// ---- backward ----
+
+int bwd_tile_dim(int d) { return d <= 64 ? 64 : 128; }
+
+// Query tiles of one key/value head: each sequence's last one may be partial.
+long long bwd_tiles(int B, int T, int G) { return T / (128 / G) + static_cast<long long>(B); }
+
+// Workspace: D and LSE * log2 e per row, then the float dQ accumulator.
+size_t bwd_stat_bytes(int B, int T, int H, int Hkv) {
+  return static_cast<size_t>(bwd_tiles(B, T, H / Hkv)) * Hkv * 128 * 4;  // a multiple of 512
+}
+
+template <typename... KArgs, typename... Args>
+bool launch_chained(void (*kern)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  // Programmatic serialisation: the kernel may be set up while the one before it on the
+  // stream finishes, and waits on the device before it reads.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess) {
+    fa2::host_count_launches(1);
+    return true;
+  }
+  cudaGetLastError();
+  return false;
+}
+
+template <int D, bool BF16>
+int launch_seq_bwd(const CUtensorMap (&m)[5], const fa2::SeqBwdParams& p, int dev, unsigned int items, cudaStream_t s) {
+  using Cfg = fa2::SeqBwdCfg<D>;
+  auto kern = fa2::fa2_seq_bwd_kernel<D, BF16>;
+  static std::atomic<bool> smem_set[kDevices];
+  if (!set_smem_once(kern, dev, Cfg::SMEM, smem_set)) return FA2_ERR_CUDA;
+  const dim3 rows(static_cast<unsigned int>(p.tiles) * (128 * D / 8 / 256), p.Hkv);
+  if (!launch_chained(fa2::fa2_seq_bwd_pre_kernel<D, BF16>, rows, 256, 0, s, p) ||
+      !launch_chained(kern, dim3(items), Cfg::THREADS, Cfg::SMEM, s, m[0], m[1], m[2], m[3], m[4], p) ||
+      !launch_chained(fa2::fa2_seq_bwd_dq_kernel<D, BF16>, rows, 256, 0, s, p))
+    return FA2_ERR_CUDA;
+  return FA2_OK;
 }
 
 }  // namespace
@@ -223,7 +268,8 @@ int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
 
 size_t fa2_bwd_varlen_workspace_size(int B, int T, int H, int Hkv, int d) {
   if (check_sizes(B, T, H, Hkv, d, kMaxBwdHeadDim) != FA2_OK) return 0;
-  return (static_cast<size_t>(H) * T * 4 + 511) / 256 * 256;
+  const size_t rows = static_cast<size_t>(bwd_tiles(B, T, H / Hkv)) * Hkv * 128;
+  return 2 * bwd_stat_bytes(B, T, H, Hkv) + rows * bwd_tile_dim(d) * 4;
 }
 
 int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V,
@@ -252,33 +298,48 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   unsigned int* st;
   rc = fa2::host_device(&dev, &n_sm, &st);
   if (rc != FA2_OK) return rc;
-  fa2::VarlenParams p{};
-  p.Q = packed(Q);
-  p.K = packed(K);
-  p.V = packed(V);
-  p.O = packed(O);
-  p.dO = packed(dO);
-  p.dQ = packed(dQ);
-  p.dK = packed(dK);
-  p.dV = packed(dV);
-  p.LSE = const_cast<float*>(LSE);
-  p.Dg = static_cast<float*>(workspace);
+  const int G = H / Hkv, tpt = 128 / G, D = bwd_tile_dim(d);
+  const long long tiles = bwd_tiles(B, T, G);
+  const long long items = (T / 128 + static_cast<long long>(std::min(B, T))) * Hkv;
+  if (tiles * 128 > 0x7fffffffll || items > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t stat = bwd_stat_bytes(B, T, H, Hkv);
+  fa2::SeqBwdParams p{};
+  p.O = static_cast<const uint16_t*>(O->data), p.o_row = O->stride_row, p.o_head = O->stride_head;
+  p.dO = static_cast<const uint16_t*>(dO->data), p.do_row = dO->stride_row, p.do_head = dO->stride_head;
+  p.dQ = static_cast<uint16_t*>(dQ->data), p.dq_row = dQ->stride_row, p.dq_head = dQ->stride_head;
+  p.dK = static_cast<uint16_t*>(dK->data), p.dk_row = dK->stride_row, p.dk_head = dK->stride_head;
+  p.dV = static_cast<uint16_t*>(dV->data), p.dv_row = dV->stride_row, p.dv_head = dV->stride_head;
+  p.LSE = LSE;
+  p.Dg = reinterpret_cast<float*>(ws);
+  p.Lg = reinterpret_cast<float*>(ws + stat);
+  p.acc = reinterpret_cast<float*>(ws + 2 * stat);
   p.cu = cu_seqlens;
   p.status = st;
-  p.B = B, p.T = T, p.H = H, p.Hkv = Hkv, p.d = d, p.causal = causal, p.window = window;
-  p.scale = scale;
-  const dim3 gq((T + 3) / 4, H), gk((T + 3) / 4, Hkv);
+  p.wait_ns = fa2::host_wait_ns();
+  p.fault = fa2::host_fault();
+  p.B = B, p.T = T, p.Hkv = Hkv, p.G = G, p.d = d, p.tpt = tpt, p.tiles = static_cast<int>(tiles);
+  p.causal = causal, p.window = std::min(window, T);  // no row sees more than T keys
+  p.scale = scale, p.scale_log2 = scale * 1.4426950408889634f;
+  // Heads to a group of the item order: at least two waves of items, and about 192 MB of the
+  // heads' rows (K, V, G times Q, dO and the float dQ), so that they stay in L2.
+  const long long per_item_head = std::max<long long>(1, items / Hkv);
+  const long long per_head = static_cast<long long>(T) * D * (4 + 8 * G);
+  const long long hg = std::max((2LL * n_sm + per_item_head - 1) / per_item_head, (192LL << 20) / std::max<long long>(1, per_head));
+  p.head_group = static_cast<int>(std::min<long long>(Hkv, std::max<long long>(1, hg)));
+  CUtensorMap m[5];
+  const uint64_t adims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(tiles) * 128, static_cast<uint64_t>(Hkv)};
+  const uint64_t astr[2] = {static_cast<uint64_t>(D) * 4, static_cast<uint64_t>(tiles) * 128 * D * 4};
+  const uint32_t abox[3] = {32, 128, 1};
+  if (!map_packed(&m[0], Q, T, H, d, dtype, false, tpt, G) || !map_packed(&m[1], K, T, Hkv, d, dtype, true, 128, 1) ||
+      !map_packed(&m[2], V, T, Hkv, d, dtype, true, 128, 1) || !map_packed(&m[3], dO, T, H, d, dtype, false, tpt, G) ||
+      !fa2::host_encode_map(&m[4], fa2::MapType::kF32, p.acc, 3, adims, astr, abox))
+    return FA2_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == FA2_BF16) {
-    fa2::fa2_varlen_dq_plain<true><<<gq, 128, 0, s>>>(p);
-    fa2::fa2_varlen_dkv_plain<true><<<gk, 128, 0, s>>>(p);
-  } else {
-    fa2::fa2_varlen_dq_plain<false><<<gq, 128, 0, s>>>(p);
-    fa2::fa2_varlen_dkv_plain<false><<<gk, 128, 0, s>>>(p);
-  }
-  if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
-  fa2::host_count_launches(2);
-  return FA2_OK;
+  const unsigned int n = static_cast<unsigned int>(items);
+  if (D == 64)
+    return dtype == FA2_BF16 ? launch_seq_bwd<64, true>(m, p, dev, n, s) : launch_seq_bwd<64, false>(m, p, dev, n, s);
+  return dtype == FA2_BF16 ? launch_seq_bwd<128, true>(m, p, dev, n, s) : launch_seq_bwd<128, false>(m, p, dev, n, s);
 }
 
 size_t fa2_fwd_paged_workspace_size(int B, int T, int H, int Hkv, int d, int sm_count) {

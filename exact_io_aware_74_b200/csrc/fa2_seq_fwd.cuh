@@ -269,41 +269,50 @@ __device__ __forceinline__ UnitAt find_unit(const SeqParams& p, long long x, int
   return r;
 }
 
-// Packed: blocks with index > level over the sequences, sum_b max(0, nblk_b - level).
-template <int QT>
-__device__ __forceinline__ int blocks_from(const SeqParams& p, int level, int lane) {
-  const int R = QT * p.tpt;
+// Packed: blocks of R rows with index >= level over the sequences, sum_b max(0, nblk_b - level).
+__device__ __forceinline__ int rows_of(const int* cu, int T, int b) {
+  const int s = min(max(cu[b], 0), T);
+  return min(max(cu[b + 1], s), T) - s;
+}
+__device__ __forceinline__ int blocks_from(const int* cu, int B, int T, int R, int level, int lane) {
   int c = 0;
-  for (int b = lane; b < p.B; b += 32) c += max(0, (seq_len(p, b).n + R - 1) / R - level);
+  for (int b = lane; b < B; b += 32) c += max(0, (rows_of(cu, T, b) + R - 1) / R - level);
   return __reduce_add_sync(0xffffffffu, c);
+}
+__device__ __forceinline__ int most_blocks(const int* cu, int B, int T, int R, int lane) {
+  int c = 0;
+  for (int b = lane; b < B; b += 32) c = max(c, (rows_of(cu, T, b) + R - 1) / R);
+  return __reduce_max_sync(0xffffffffu, c);
 }
 
 // Packed: item w of the order -- head group by head group, in a group the blocks of the
-// highest index (the most keys, when causal) of all sequences first, heads innermost.
-// False when there are fewer items.  Whole warp.
-template <int QT>
-__device__ __forceinline__ bool find_item(const SeqParams& p, int w, int n_blocks, int max_blk, int lane,
-                                          SeqItem& it) {
-  if (w >= n_blocks * p.Hkv) return false;
-  const int per = p.head_group * n_blocks, grp = w / per, at = w - grp * per;
-  const int heads = min(p.head_group, p.Hkv - grp * p.head_group);
-  const int rank = at / heads, kvh = grp * p.head_group + at % heads;
+// highest level of all sequences first, heads innermost.  False when there are fewer
+// items (n_blocks to a head, at most max_blk to a sequence).  Whole warp.
+struct BlockAt {
+  int b, level, kvh;
+};
+__device__ __forceinline__ bool find_block(const int* cu, int B, int T, int Hkv, int head_group, int R, int w,
+                                           int n_blocks, int max_blk, int lane, BlockAt& r) {
+  if (w >= static_cast<long long>(n_blocks) * Hkv) return false;
+  const int per = head_group * n_blocks, grp = w / per, at = w - grp * per;
+  const int heads = min(head_group, Hkv - grp * head_group);
+  const int rank = at / heads;
+  r.kvh = grp * head_group + at % heads;
   int lo = 0, hi = max_blk;  // the largest level with blocks_from(level) > rank
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (blocks_from<QT>(p, mid, lane) > rank) lo = mid; else hi = mid;
+    if (blocks_from(cu, B, T, R, mid, lane) > rank) lo = mid; else hi = mid;
   }
-  int i = rank - blocks_from<QT>(p, lo + 1, lane);  // the i-th sequence with more than lo blocks
-  const int R = QT * p.tpt;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
+  r.level = lo;
+  int i = rank - blocks_from(cu, B, T, R, lo + 1, lane);  // the i-th sequence with more than lo blocks
+  for (int b0 = 0; b0 < B; b0 += 32) {
     const int b = b0 + lane;
-    const bool has = b < p.B && (seq_len(p, b).n + R - 1) / R > lo;
+    const bool has = b < B && (rows_of(cu, T, b) + R - 1) / R > lo;
     const unsigned int m = __ballot_sync(0xffffffffu, has);
     const int c = __popc(m);
     if (i < c) {
       const bool mine = has && __popc(m & ((1u << lane) - 1u)) == i;
-      const int l = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-      make_item<QT>(p, seq_len(p, b0 + l), b0 + l, kvh, lo, it);
+      r.b = b0 + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
       return true;
     }
     i -= c;
@@ -473,12 +482,15 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
       } else {
-        int mb = 0;
-        for (int b = lane; b < p.B; b += 32) mb = max(mb, (seq_len(p, b).n + QT * p.tpt - 1) / (QT * p.tpt));
-        const int max_blk = __reduce_max_sync(0xffffffffu, mb), n_blocks = blocks_from<QT>(p, 0, lane);
+        const int R = QT * p.tpt;
+        const int max_blk = most_blocks(p.cu, p.B, p.T, R, lane), n_blocks = blocks_from(p.cu, p.B, p.T, R, 0, lane);
+        BlockAt at;
         int w = blockIdx.x;
         for (int k = 0; ok && w >= 0; ++k) {
-          if (find_item<QT>(p, w, n_blocks, max_blk, lane, it)) ok = publish(it);
+          if (find_block(p.cu, p.B, p.T, p.Hkv, p.head_group, R, w, n_blocks, max_blk, lane, at)) {
+            make_item<QT>(p, seq_len(p, at.b), at.b, at.kvh, at.level, it);
+            ok = publish(it);
+          }
           // The next index only once the item before this one is done with: a CTA holds
           // at most one item that it has not begun.
           if (ok && ii >= 2)

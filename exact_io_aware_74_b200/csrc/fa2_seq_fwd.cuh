@@ -665,163 +665,138 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       __syncwarp();
     } else if (lane == 0) {
       // ---------------------------------------------------------------- MMA issuer (warp 9)
+      // One loop over the key tiles of all items.  Step j issues P V of its own tile and S of
+      // the step after it, which may be the next item's first; the loop begins with a step
+      // that has no P V.  (One thread feeds the tensor pipe: a body with every product once
+      // keeps it in the instruction cache and its state in registers.)
       constexpr uint32_t id_qk = idesc_f16(128, 128, BF16, false, false);
       constexpr uint32_t id_pv = idesc_f16(128, D, BF16, false, true);
-      const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_u32(sV), C::CHUNK, 1024);
       int ii = 0, qc = 0, kc = 0, vc = 0;
-      int sc[2] = {0, 0};   // score products issued per tile
-      int ic[2] = {0, 0};   // items begun per tile
-      struct Cur {
-        int lo[2], hi[2], qs[2], j0, n;
-      };
-      // The next item with key tiles: 1, or 0 at the end and -1 on a timeout.
-      auto fetch = [&](Cur& c) -> int {
-        for (;; ) {
-          const int s = ii % NI;
-          if (!mbar_wait(&item_full[s], (ii / NI) & 1, wc, kQSiteItem)) return -1;
-          const SeqItem& it = items[s];
-          const bool valid = it.valid != 0;
-          c.lo[0] = it.lo[0], c.lo[1] = it.lo[1], c.hi[0] = it.hi[0], c.hi[1] = it.hi[1];
-          c.j0 = it.j0, c.n = it.n;
-          mbar_arrive(&item_empty[s]);
-          ++ii;
-          if (!valid) return 0;
-          if (c.n == 0) continue;
-#pragma unroll
-          for (int t = 0; t < QT; ++t)
-            if (c.hi[t] > 0) c.qs[t] = qc++;
-          return 1;
-        }
-      };
-      // S of tile t (Q load number q) against K slot ks.
-      auto issue_s = [&](int t, int q, int ks, bool last) {
-        const int b = QT == 2 ? t : (sc[0] & 1);
-        const uint32_t dt = tbase + b * 128, qa = aQ + (q % C::QS) * C::TILE, ka = aK + ks * C::TILE;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-          umma_ss(dt, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_qk, kk > 0);
-        }
-        umma_commit(&s_full[b]);
-        if (last) umma_commit(&q_empty[q % C::QS]);
-        ++sc[t];
-      };
-      auto issue_pv = [&](int t, uint32_t a_col, int vs, bool acc) {
-        const uint32_t va = aV + vs * C::TILE, dt = tbase + C::O_COL(t);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts(dt, tbase + a_col + kk * 8, sdesc_sw128(va + kk * 2048, C::CHUNK, 1024), id_pv,
-                  (acc || kk > 0) ? 1u : 0u);
-        umma_commit(&o_done[t]);
-        umma_commit(&v_empty[vs]);
-      };
-      Cur cur{}, nxt{};
-      int have = fetch(cur);
-      bool ok = have >= 0;
-      // First scores of an item's tile t; k_ok: K has been waited for.
-      auto first_s = [&](const Cur& c, int t, bool& k_ok) -> bool {
-        if (c.hi[t] == 0 || c.lo[t] != c.j0) return true;
-        const int q = c.qs[t];
-        if (!mbar_wait(&q_full[q % C::QS], (q / C::QS) & 1, wc, kQSiteMmaQ)) return false;
-        if (!k_ok && !mbar_wait(&k_full[kc % C::KS], (kc / C::KS) & 1, wc, kQSiteMmaK)) return false;
-        k_ok = true;
-        if (C::SEP && sc[t] > 0 && !mbar_wait(&s_free[t], (sc[t] - 1) & 1, wc, kQSiteMmaP)) return false;
-        tc_fence_after();
-        issue_s(t, q, kc % C::KS, c.hi[t] == c.j0 + 1);
-        return true;
-      };
-      if (have == 1) {
-        bool k_ok = false;
-        for (int t = 0; t < QT && ok; ++t) ok = first_s(cur, t, k_ok);
-        if (ok) {
-          umma_commit(&k_empty[kc % C::KS]);
-          ++kc;
-        }
-      }
-      while (ok && have == 1) {
-        int more = 1;
-        for (int jj = 0; jj < cur.n && ok; ++jj, ++vc) {
-          const int j = cur.j0 + jj, vs = vc % C::VS;
-          const bool last = jj + 1 == cur.n;
-          bool k_ok = false, v_ok = false, fetched = false;
-          // S of the step after this one: this item's next key tile or the next item's first.
-          auto next_s = [&](int t) -> bool {
-            if (last) {
-              if (!fetched) {
-                more = fetch(nxt);
-                fetched = true;
-                if (more < 0) return false;
-              }
-              return more != 1 || first_s(nxt, t, k_ok);
-            }
-            if (j + 1 < cur.lo[t] || j + 1 >= cur.hi[t]) return true;
-            if (!k_ok && !mbar_wait(&k_full[kc % C::KS], (kc / C::KS) & 1, wc, kQSiteMmaK)) return false;
-            k_ok = true;
-            const int q = cur.qs[t];
-            if (j + 1 == cur.lo[t] && !mbar_wait(&q_full[q % C::QS], (q / C::QS) & 1, wc, kQSiteMmaQ)) return false;
-            if (C::SEP && sc[t] > 0 && !mbar_wait(&s_free[t], (sc[t] - 1) & 1, wc, kQSiteMmaP)) return false;
-            tc_fence_after();
-            issue_s(t, q, kc % C::KS, j + 2 == cur.hi[t]);
-            return true;
-          };
-          // O_t += P_t V.  pc: number of the product (its P is phase pc).
-          auto pv = [&](int t) -> bool {
-            if (j < cur.lo[t] || j >= cur.hi[t]) return true;
-            const bool first = j == cur.lo[t];
-            if (!v_ok && !mbar_wait(&v_full[vs], (vc / C::VS) & 1, wc, kQSiteMmaV)) return false;
-            v_ok = true;
-            if (first) {
-              // The item before has read its output out of the accumulator.
-              if (ic[t] > 0 && !mbar_wait(&o_free[t], (ic[t] - 1) & 1, wc, kQSiteMmaO)) return false;
-              ++ic[t];
-            }
-            return true;
-          };
-          if constexpr (QT == 1) {
-            // S of the next step goes ahead of this step's P: two S blocks in turn.
-            const int pc = sc[0] - 1;
-            ok = next_s(0);
-            if (!ok) break;
-            if (!last || more == 1) {
-              umma_commit(&k_empty[kc % C::KS]);
-              ++kc;
-            }
-            ok = pv(0) && mbar_wait(&p_ready[pc & 1], (pc >> 1) & 1, wc, kQSiteMmaP);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(0, (pc & 1) * 128, vs, j > cur.lo[0]);
-          } else {
-            auto do_pv = [&](int t, int pc) -> bool {
-              if (!pv(t)) return false;
-              if (j < cur.lo[t] || j >= cur.hi[t]) return true;
-              if (!mbar_wait(&p_ready[t], pc & 1, wc, kQSiteMmaP)) return false;
-              tc_fence_after();
-              const uint32_t va = aV + vs * C::TILE, dt = tbase + C::O_COL(t);
-              const uint32_t a_col = C::SEP ? C::P_COL(t) : t * 128u;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_ts(dt, tbase + a_col + kk * 8, sdesc_sw128(va + kk * 2048, C::CHUNK, 1024), id_pv,
-                        (j > cur.lo[t] || kk > 0) ? 1u : 0u);
-              umma_commit(&o_done[t]);
-              return true;
-            };
-            const int p0 = sc[0] - 1, p1 = sc[1] - 1;
-            if constexpr (C::SEP) ok = next_s(0) && next_s(1) && do_pv(0, p0) && do_pv(1, p1);
-            else ok = do_pv(0, p0) && next_s(0) && do_pv(1, p1) && next_s(1);
-            // A slot is only released once its load has landed.
-            if (ok && !v_ok) ok = mbar_wait(&v_full[vs], (vc / C::VS) & 1, wc, kQSiteMmaV);
-            const bool adv = !last || more == 1;
-            if (ok && adv && !k_ok) ok = mbar_wait(&k_full[kc % C::KS], (kc / C::KS) & 1, wc, kQSiteMmaK);
-            if (!ok) break;
-            umma_commit(&v_empty[vs]);
-            if (adv) {
-              umma_commit(&k_empty[kc % C::KS]);
-              ++kc;
-            }
+      int sc0 = 0, sc1 = 0;  // score products issued per tile
+      int ic0 = 0, ic1 = 0;  // items begun per tile
+      int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0, q0 = 0, q1 = 0;  // the item: key tiles and Q loads
+      int j = -1, jend = 0;
+      bool ok = true;
+      while (ok) {
+        const bool real = j >= 0, last = j + 1 == jend;
+        const int vs = vc % C::VS, ks = kc % C::KS;
+        bool k_ok = false, v_ok = false, more = true;
+        const SeqItem* nx = nullptr;
+        // The next item that has key tiles; more: there is one.
+        auto fetch = [&]() {
+          for (;; ++ii) {
+            nx = &items[ii % NI];
+            if (!mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem)) { ok = false; return; }
+            more = nx->valid != 0;
+            if (!more || nx->n > 0) return;
+            mbar_arrive(&item_empty[ii % NI]);
           }
+        };
+        // S of tile t for the step after this one.
+        auto next_s = [&](int t, int lo, int hi, int q, int& sc) {
+          bool go, need_q, fin;
+          if (!last) {
+            go = j + 1 >= lo && j + 1 < hi;
+            need_q = j + 1 == lo;
+            fin = j + 2 == hi;
+          } else {
+            if (!more) return;
+            const int nlo = nx->lo[t], nhi = nx->hi[t];
+            go = nhi > 0 && nlo == nx->j0;
+            need_q = true;
+            fin = nhi == nlo + 1;
+            q = qc + (t == 1 && nx->hi[0] > 0 ? 1 : 0);
+          }
+          if (!go) return;
+          const int qs = q % C::QS;
+          if (need_q) ok = mbar_wait(&q_full[qs], (q / C::QS) & 1, wc, kQSiteMmaQ);
+          if (ok && !k_ok) ok = mbar_wait(&k_full[ks], (kc / C::KS) & 1, wc, kQSiteMmaK);
+          // The S block holds the step before's scores until they have been read.
+          if (ok && C::SEP && sc > 0) ok = mbar_wait(&s_free[t], (sc - 1) & 1, wc, kQSiteMmaP);
+          if (!ok) return;
+          k_ok = true;
+          tc_fence_after();
+          const int b = QT == 2 ? t : (sc & 1);
+          const uint64_t da = sdesc_add(dQ, qs * C::TILE), db = sdesc_add(dK, ks * C::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+            umma_ss(tbase + b * 128, sdesc_add(da, off), sdesc_add(db, off), id_qk, kk > 0);
+          }
+          umma_commit(&s_full[b]);
+          if (fin) umma_commit(&q_empty[qs]);
+          ++sc;
+        };
+        // O_t += P V; pc: number of the step's scores.
+        auto pv = [&](int t, int lo, int hi, int pc, int& ic) {
+          if (j < lo || j >= hi) return;
+          if (!v_ok) ok = mbar_wait(&v_full[vs], (vc / C::VS) & 1, wc, kQSiteMmaV);
+          if (!ok) return;
+          v_ok = true;
+          // An item's first product overwrites the accumulator: read out by then.
+          if (j == lo) {
+            if (ic > 0) ok = mbar_wait(&o_free[t], (ic - 1) & 1, wc, kQSiteMmaO);
+            ++ic;
+          }
+          const int pb = QT == 2 ? t : (pc & 1);
+          if (ok) ok = mbar_wait(&p_ready[pb], (QT == 2 ? pc : pc >> 1) & 1, wc, kQSiteMmaP);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t db = sdesc_add(dV, vs * C::TILE);
+          const uint32_t at = tbase + (C::SEP ? C::P_COL(t) : pb * 128u);
+          const uint32_t acc = j > lo ? 1u : 0u;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tbase + C::O_COL(t), at + kk * 8, sdesc_add(db, kk * 2048), id_pv, kk > 0 ? 1u : acc);
+          umma_commit(&o_done[t]);
+        };
+        auto k_done = [&]() {  // a slot is only released once its load has landed
+          if (last && !more) return;
+          if (QT == 2 && !k_ok) ok = mbar_wait(&k_full[ks], (kc / C::KS) & 1, wc, kQSiteMmaK);
+          if (!ok) return;
+          umma_commit(&k_empty[ks]);
+          ++kc;
+        };
+        const int p0 = sc0 - 1, p1 = sc1 - 1;
+        if constexpr (QT == 1) {
+          // S of the next step goes ahead of this step's P: two S blocks in turn.
+          if (last) fetch();
+          if (ok) next_s(0, lo0, hi0, q0, sc0);
+          if (ok) k_done();
+          if (ok) pv(0, lo0, hi0, p0, ic0);
+        } else if constexpr (C::SEP) {
+          if (last) fetch();
+          if (ok) next_s(0, lo0, hi0, q0, sc0);
+          if (ok) next_s(1, lo1, hi1, q1, sc1);
+          if (ok) pv(0, lo0, hi0, p0, ic0);
+          if (ok) pv(1, lo1, hi1, p1, ic1);
+          if (ok) k_done();
+        } else {
+          pv(0, lo0, hi0, p0, ic0);
+          if (ok && last) fetch();
+          if (ok) next_s(0, lo0, hi0, q0, sc0);
+          if (ok) pv(1, lo1, hi1, p1, ic1);
+          if (ok) next_s(1, lo1, hi1, q1, sc1);
+          if (ok) k_done();
         }
-        have = ok ? more : -1;
-        cur = nxt;
+        if (!ok) break;
+        if (real) {
+          if (QT == 2 && !v_ok && !mbar_wait(&v_full[vs], (vc / C::VS) & 1, wc, kQSiteMmaV)) break;
+          umma_commit(&v_empty[vs]);
+          ++vc;
+        }
+        ++j;
+        if (!last) continue;
+        if (!more) break;
+        lo0 = nx->lo[0], hi0 = nx->hi[0], lo1 = nx->lo[1], hi1 = nx->hi[1];
+        j = nx->j0;
+        jend = j + nx->n;
+        if (hi0 > 0) q0 = qc++;
+        if (QT == 2 && hi1 > 0) q1 = qc++;
+        mbar_arrive(&item_empty[ii % NI]);
+        ++ii;
       }
       // Every product issued completes before tensor memory is released.
       umma_commit(&drain);

@@ -50,6 +50,10 @@ bool cache_ok(const fa2_cache* x, int blocks, int heads, int rows, int d) {
          (heads <= 1 || stride_ok(x->stride_head, d)) && (rows <= 1 || stride_ok(x->stride_row, d));
 }
 
+// Sequences that may hold a partial block: the empty ones too where the order of the blocks
+// keeps a place for each (BlockOrder).
+int partial_blocks(int B, int T) { return B > fa2::kHeld ? B : std::min(B, T); }
+
 // ---- forward over packed sequences and paged caches ----
 
 int fwd_tile_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
@@ -250,7 +254,7 @@ int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   const int G = H / Hkv, tpt = 128 / G;
   // Items there could be: every sequence's last block may be partial.
   const auto items = [&](int qt) {
-    return (static_cast<long long>(T) / (qt * tpt) + std::min(B, T)) * Hkv;
+    return (static_cast<long long>(T) / (qt * tpt) + partial_blocks(B, T)) * Hkv;
   };
   // Two query tiles to a CTA; one (twice the CTAs) where two would leave SMs without work.
   const int qt = d <= 128 && items(2) >= n_sm ? 2 : 1;
@@ -300,7 +304,7 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   if (rc != FA2_OK) return rc;
   const int G = H / Hkv, tpt = 128 / G, D = bwd_tile_dim(d);
   const long long tiles = bwd_tiles(B, T, G);
-  const long long items = (T / 128 + static_cast<long long>(std::min(B, T))) * Hkv;
+  const long long items = (T / 128 + static_cast<long long>(partial_blocks(B, T))) * Hkv;
   if (tiles * 128 > 0x7fffffffll || items > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t stat = bwd_stat_bytes(B, T, H, Hkv);

@@ -265,11 +265,12 @@ fa2_seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       ++ii;
       return true;
     };
-    const int max_blk = most_blocks(p.cu, p.B, p.T, 128, lane), n_blocks = blocks_from(p.cu, p.B, p.T, 128, 0, lane);
+    BlockOrder order;
+    order.load(p.cu, p.B, p.T, 128, lane);
     int w = blockIdx.x;
     BlockAt at;
     for (int k = 0; ok && w >= 0; ++k) {
-      if (find_block(p.cu, p.B, p.T, p.Hkv, p.head_group, 128, w, n_blocks, max_blk, lane, at)) {
+      if (order.find(p.cu, p.B, p.T, p.Hkv, p.head_group, 128, w, lane, at)) {
         it.row0 = min(max(p.cu[at.b], 0), p.T);
         it.n = rows_of(p.cu, p.T, at.b);
         it.kvh = at.kvh;

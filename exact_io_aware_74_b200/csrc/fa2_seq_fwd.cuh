@@ -87,6 +87,7 @@ enum SeqSite : uint32_t {
 };
 
 constexpr int kSeqItems = 4;  // ring of items handed to the roles
+constexpr int kHeld = 256;    // sequences whose lengths a scheduling warp holds in registers
 
 struct SeqItem {
   int row0, n_tok;   // first packed query row, tokens
@@ -174,25 +175,19 @@ __device__ __forceinline__ int block_units(const SeqParams& p, const SeqLen& s, 
   return max(1, max(h0, h1) - lo);
 }
 
-// Units of one key/value head of the sequences b0 + lane (0 past B): lanes with few
-// blocks sum their own, the others' are summed by the whole warp.
+// Units of one key/value head of a sequence per lane: lanes with few blocks sum their own,
+// the others' are summed by the whole warp.
 template <int QT>
-__device__ __forceinline__ int chunk_units(const SeqParams& p, int b0, int lane) {
-  const int b = b0 + lane;
-  SeqLen s{0, 0, 0};
-  if (b < p.B) s = seq_len(p, b);
-  const int R = QT * p.tpt, nb = (s.n + R - 1) / R;
+__device__ __forceinline__ int lane_units(const SeqParams& p, int n, int nk, int lane) {
+  const int R = QT * p.tpt, nb = (n + R - 1) / R;
   int u = 0;
   if (nb <= 4)
-    for (int i = 0; i < nb; ++i) u += block_units<QT>(p, s, i);
+    for (int i = 0; i < nb; ++i) u += block_units<QT>(p, SeqLen{0, n, nk}, i);
   unsigned int many = __ballot_sync(0xffffffffu, nb > 4);
   while (many) {
     const int l = __ffs(many) - 1;
     many &= many - 1;
-    SeqLen o;
-    o.row0 = 0;
-    o.n = __shfl_sync(0xffffffffu, s.n, l);
-    o.nk = __shfl_sync(0xffffffffu, s.nk, l);
+    const SeqLen o{0, __shfl_sync(0xffffffffu, n, l), __shfl_sync(0xffffffffu, nk, l)};
     int part = 0;
     for (int i = lane; i < (o.n + R - 1) / R; i += 32) part += block_units<QT>(p, o, i);
     part = __reduce_add_sync(0xffffffffu, part);
@@ -210,14 +205,6 @@ __device__ __forceinline__ int warp_inclusive(int x, int lane) {
   return x;
 }
 
-// Total units of all heads (whole warp; every lane gets the sum).
-template <int QT>
-__device__ __forceinline__ long long total_units(const SeqParams& p, int lane) {
-  long long w = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) w += __reduce_add_sync(0xffffffffu, chunk_units<QT>(p, b0, lane));
-  return w * p.Hkv;
-}
-
 // CTAs that get a share: at least kMinUnits units each.
 constexpr int kMinUnits = 2;
 __device__ __forceinline__ int share_ctas(long long units, int grid) {
@@ -226,99 +213,173 @@ __device__ __forceinline__ int share_ctas(long long units, int grid) {
 }
 __device__ __forceinline__ long long share_start(long long units, int ctas, int c) { return units * c / ctas; }
 
-// Where unit x of the linear order (sequence, head, block, key tile) lies.  Whole warp.
+// The linear order of the units: sequence, head, block, key tile.  Whole warp; up to kHeld
+// sequences' units stay in registers between the total and the search.
 struct UnitAt {
   int b, kvh, blk, at;  // at: units of the block before x
-  int units;            // of one head of the sequence
   SeqLen s;
 };
 template <int QT>
-__device__ __forceinline__ UnitAt find_unit(const SeqParams& p, long long x, int lane) {
-  UnitAt r{};
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int u = chunk_units<QT>(p, b0, lane);
-    const int inc = warp_inclusive(u, lane);
-    const long long end = static_cast<long long>(inc) * p.Hkv;
-    const unsigned int m = __ballot_sync(0xffffffffu, end > x);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      r.b = b0 + l;
-      r.units = __shfl_sync(0xffffffffu, u, l);
-      x -= __shfl_sync(0xffffffffu, end, l) - static_cast<long long>(r.units) * p.Hkv;
-      break;
-    }
-    x -= __shfl_sync(0xffffffffu, end, 31);
-  }
-  r.s = seq_len(p, r.b);
-  r.kvh = static_cast<int>(x / r.units);
-  int rem = static_cast<int>(x - static_cast<long long>(r.kvh) * r.units);
-  const int R = QT * p.tpt, nb = (r.s.n + R - 1) / R;
-  for (int i0 = 0; i0 < nb; i0 += 32) {
-    const int u = i0 + lane < nb ? block_units<QT>(p, r.s, i0 + lane) : 0;
-    const int inc = warp_inclusive(u, lane);
-    const unsigned int m = __ballot_sync(0xffffffffu, inc > rem);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      r.blk = i0 + l;
-      rem -= __shfl_sync(0xffffffffu, inc - u, l);
-      break;
-    }
-    rem -= __shfl_sync(0xffffffffu, inc, 31);
-  }
-  r.at = rem;
-  return r;
-}
+struct UnitOrder {
+  int u[kHeld / 32];
+  long long total;  // of all heads
 
-// Packed: blocks of R rows with index >= level over the sequences, sum_b max(0, nblk_b - level).
+  __device__ __forceinline__ int chunk(const SeqParams& p, int b0, int lane) const {
+    SeqLen s{0, 0, 0};
+    if (b0 + lane < p.B) s = seq_len(p, b0 + lane);
+    return lane_units<QT>(p, s.n, s.nk, lane);
+  }
+  __device__ __forceinline__ void load(const SeqParams& p, int lane) {
+    total = 0;
+    if (p.B > kHeld) {
+      for (int b0 = 0; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, chunk(p, b0, lane));
+    } else {
+      int n[kHeld / 32], nk[kHeld / 32];  // all loads before the first use
+#pragma unroll
+      for (int i = 0; i < kHeld / 32; ++i) {
+        SeqLen s{0, 0, 0};
+        if (i * 32 + lane < p.B) s = seq_len(p, i * 32 + lane);
+        n[i] = s.n, nk[i] = s.nk;
+      }
+#pragma unroll
+      for (int i = 0; i < kHeld / 32; ++i) {
+        u[i] = i * 32 < p.B ? lane_units<QT>(p, n[i], nk[i], lane) : 0;
+        total += __reduce_add_sync(0xffffffffu, u[i]);
+      }
+    }
+    total *= p.Hkv;
+  }
+  // Unit x < total.
+  __device__ __forceinline__ UnitAt find(const SeqParams& p, long long x, int lane) const {
+    UnitAt r{};
+    int units = 1;  // of one head of the sequence
+    bool found = false;
+    auto look = [&](int b0, int v) {
+      const int inc = warp_inclusive(v, lane);
+      const long long end = static_cast<long long>(inc) * p.Hkv;
+      const unsigned int m = __ballot_sync(0xffffffffu, end > x);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        r.b = b0 + l;
+        units = __shfl_sync(0xffffffffu, v, l);
+        x -= __shfl_sync(0xffffffffu, end, l) - static_cast<long long>(units) * p.Hkv;
+        found = true;
+      } else {
+        x -= __shfl_sync(0xffffffffu, end, 31);
+      }
+    };
+    if (p.B > kHeld) {
+      for (int b0 = 0; b0 < p.B && !found; b0 += 32) look(b0, chunk(p, b0, lane));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kHeld / 32; ++i)
+        if (!found && i * 32 < p.B) look(i * 32, u[i]);
+    }
+    r.s = seq_len(p, r.b);
+    r.kvh = static_cast<int>(x / units);
+    int rem = static_cast<int>(x - static_cast<long long>(r.kvh) * units);
+    const int R = QT * p.tpt, nb = (r.s.n + R - 1) / R;
+    for (int i0 = 0; i0 < nb; i0 += 32) {
+      const int v = i0 + lane < nb ? block_units<QT>(p, r.s, i0 + lane) : 0;
+      const int inc = warp_inclusive(v, lane);
+      const unsigned int m = __ballot_sync(0xffffffffu, inc > rem);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        r.blk = i0 + l;
+        rem -= __shfl_sync(0xffffffffu, inc - v, l);
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    r.at = rem;
+    return r;
+  }
+};
+
 __device__ __forceinline__ int rows_of(const int* cu, int T, int b) {
   const int s = min(max(cu[b], 0), T);
   return min(max(cu[b + 1], s), T) - s;
 }
-__device__ __forceinline__ int blocks_from(const int* cu, int B, int T, int R, int level, int lane) {
-  int c = 0;
-  for (int b = lane; b < B; b += 32) c += max(0, (rows_of(cu, T, b) + R - 1) / R - level);
-  return __reduce_add_sync(0xffffffffu, c);
-}
-__device__ __forceinline__ int most_blocks(const int* cu, int B, int T, int R, int lane) {
-  int c = 0;
-  for (int b = lane; b < B; b += 32) c = max(c, (rows_of(cu, T, b) + R - 1) / R);
-  return __reduce_max_sync(0xffffffffu, c);
-}
 
-// Packed: item w of the order -- head group by head group, in a group the blocks of the
-// highest level of all sequences first, heads innermost.  False when there are fewer
-// items (n_blocks to a head, at most max_blk to a sequence).  Whole warp.
+// Packed: the order of the items, found by one warp.  Up to kHeld sequences their block
+// counts sit in registers, and the order is head group by head group, in a group the
+// blocks of the highest level (index from the sequence's start) of all sequences first,
+// heads innermost: heaviest first, when causal.  With more sequences the blocks lie
+// sequence by sequence, highest first (cu[b] / R + b is where sequence b's start: its last
+// block may be partial, so some places hold none).  Searching the counts in memory for the
+// first order took 5 to 9 us an item with 148 and 740 sequences (B200); either of these
+// takes well under 1.
 struct BlockAt {
   int b, level, kvh;
 };
-__device__ __forceinline__ bool find_block(const int* cu, int B, int T, int Hkv, int head_group, int R, int w,
-                                           int n_blocks, int max_blk, int lane, BlockAt& r) {
-  if (w >= static_cast<long long>(n_blocks) * Hkv) return false;
-  const int per = head_group * n_blocks, grp = w / per, at = w - grp * per;
-  const int heads = min(head_group, Hkv - grp * head_group);
-  const int rank = at / heads;
-  r.kvh = grp * head_group + at % heads;
-  int lo = 0, hi = max_blk;  // the largest level with blocks_from(level) > rank
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (blocks_from(cu, B, T, R, mid, lane) > rank) lo = mid; else hi = mid;
-  }
-  r.level = lo;
-  int i = rank - blocks_from(cu, B, T, R, lo + 1, lane);  // the i-th sequence with more than lo blocks
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    const bool has = b < B && (rows_of(cu, T, b) + R - 1) / R > lo;
-    const unsigned int m = __ballot_sync(0xffffffffu, has);
-    const int c = __popc(m);
-    if (i < c) {
-      const bool mine = has && __popc(m & ((1u << lane) - 1u)) == i;
-      r.b = b0 + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-      return true;
+
+struct BlockOrder {
+  int nb[kHeld / 32];   // blocks of sequences lane, lane + 32, ...
+  int n_blocks, max_blk;  // of one head; of one sequence
+
+  __device__ __forceinline__ void load(const int* cu, int B, int T, int R, int lane) {
+    if (B > kHeld) {
+      n_blocks = T / R + B;
+      return;
     }
-    i -= c;
+    int sum = 0, most = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld / 32; ++i) {
+      const int b = i * 32 + lane;
+      nb[i] = b < B ? (rows_of(cu, T, b) + R - 1) / R : 0;
+      sum += nb[i];
+      most = max(most, nb[i]);
+    }
+    n_blocks = __reduce_add_sync(0xffffffffu, sum);
+    max_blk = __reduce_max_sync(0xffffffffu, most);
   }
-  return false;
-}
+  __device__ __forceinline__ int from(int level) const {  // blocks of that level and above
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld / 32; ++i) c += max(0, nb[i] - level);
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+  // Item w (whole warp); false when the place holds none.
+  __device__ __forceinline__ bool find(const int* cu, int B, int T, int Hkv, int head_group, int R, int w, int lane,
+                                       BlockAt& r) const {
+    if (w >= static_cast<long long>(n_blocks) * Hkv) return false;
+    const int per = head_group * n_blocks, grp = w / per, at = w - grp * per;
+    const int heads = min(head_group, Hkv - grp * head_group);
+    const int rank = at / heads;
+    r.kvh = grp * head_group + at - rank * heads;
+    if (B > kHeld) {
+      int lo = 0, n = B;  // the last sequence whose place is at or before rank is in [lo, lo + n)
+      while (n > 1) {
+        const int step = (n + 31) / 32, b = lo + lane * step;
+        const bool le = lane * step < n && min(max(cu[b], 0), T) / R + b <= rank;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+        lo += k * step;
+        n = min(step, n - k * step);
+      }
+      r.b = lo;
+      const int blocks = (rows_of(cu, T, lo) + R - 1) / R;
+      r.level = blocks - 1 - (rank - (min(max(cu[lo], 0), T) / R + lo));
+      return r.level >= 0 && r.level < blocks;
+    }
+    int lo = 0, hi = max_blk;  // the largest level with from(level) > rank
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (from(mid) > rank) lo = mid; else hi = mid;
+    }
+    r.level = lo;
+    int i = rank - from(lo + 1);  // the i-th sequence with more than lo blocks
+    r.b = -1;
+#pragma unroll
+    for (int c = 0; c < kHeld / 32; ++c) {
+      const bool has = nb[c] > lo;
+      const unsigned int m = __ballot_sync(0xffffffffu, has);
+      const unsigned int hit = __ballot_sync(0xffffffffu, has && __popc(m & ((1u << lane) - 1u)) == i);
+      if (r.b < 0 && hit) r.b = c * 32 + __ffs(hit) - 1;
+      i -= __popc(m);
+    }
+    return r.b >= 0;
+  }
+};
 
 // ------------------------------------------------------------------------------------
 // cluster launch control: the index of a CTA of this grid that has not started
@@ -453,12 +514,14 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       SeqItem it{};
       bool ok = true;
       if (paged) {
-        const long long units = total_units<QT>(p, lane);
+        UnitOrder<QT> order;
+        order.load(p, lane);
+        const long long units = order.total;
         const int ctas = share_ctas(units, gridDim.x), c = blockIdx.x;
         long long x = share_start(units, ctas, c);
         const long long xe = c < ctas ? share_start(units, ctas, c + 1) : x;
         if (x < xe) {
-          UnitAt u = find_unit<QT>(p, x, lane);
+          UnitAt u = order.find(p, x, lane);
           const int R = QT * p.tpt;
           while (ok) {
             const int len = block_units<QT>(p, u.s, u.blk);
@@ -483,11 +546,12 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
       } else {
         const int R = QT * p.tpt;
-        const int max_blk = most_blocks(p.cu, p.B, p.T, R, lane), n_blocks = blocks_from(p.cu, p.B, p.T, R, 0, lane);
+        BlockOrder order;
+        order.load(p.cu, p.B, p.T, R, lane);
         BlockAt at;
         int w = blockIdx.x;
         for (int k = 0; ok && w >= 0; ++k) {
-          if (find_block(p.cu, p.B, p.T, p.Hkv, p.head_group, R, w, n_blocks, max_blk, lane, at)) {
+          if (order.find(p.cu, p.B, p.T, p.Hkv, p.head_group, R, w, lane, at)) {
             make_item<QT>(p, seq_len(p, at.b), at.b, at.kvh, at.level, it);
             ok = publish(it);
           }
@@ -1034,11 +1098,13 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 template <int D, bool BF16, int QT>
 __global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p, int grid) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long units = total_units<QT>(p, lane);
+  UnitOrder<QT> order;
+  order.load(p, lane);
+  const long long units = order.total;
   const int ctas = share_ctas(units, grid), c = blockIdx.x + 1;
   if (c >= ctas || units == 0) return;
   const long long x = share_start(units, ctas, c);
-  const UnitAt u = find_unit<QT>(p, x, lane);
+  const UnitAt u = order.find(p, x, lane);
   if (u.at == 0 || share_start(units, ctas, c - 1) > x - u.at) return;
   const long long end = x - u.at + block_units<QT>(p, u.s, u.blk);
   int last = c;  // the last share with a part of the block

@@ -4,6 +4,7 @@ Bounds: see packed_ref.py.
 """
 
 import math
+import random
 
 import pytest
 import torch
@@ -91,6 +92,22 @@ def test_backward(lens, d, causal, window):
 def test_backward_head_groups_and_dims(H, Hk, d, dtype):
     check_backward([3, 200, 131, 0, 1], H, Hk, d, dtype, True, 0, seed=H + d)
     check_backward([140, 20], H, Hk, d, dtype, False, 0, seed=H + d + 1)
+
+
+@pytest.mark.parametrize("B", [255, 256, 257, 700])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_sequences(B, d):
+    """More sequences than a scheduling warp holds in registers, empty ones among them."""
+    r = random.Random(B)
+    lens = [r.choice([0, 0, 1, 2, 7, 40]) for _ in range(B)]
+    lens[B // 2] = 700
+    lens[-1] = r.choice([0, 150])
+    check_forward(lens, 2, 1, d, "bf16", True, 0, seed=B)
+    check_backward(lens, 2, 1, d, "bf16", True, 0, seed=B + 1)
+    few = [0] * B
+    few[B // 3], few[-2] = 2, 1  # far more sequences than rows
+    check_forward(few, 2, 2, d, "bf16", True, 0, seed=B + 2)
+    check_backward(few, 2, 2, d, "bf16", False, 0, seed=B + 3)
 
 
 def test_gradients_are_the_slopes_of_the_loss():

@@ -7,10 +7,6 @@
 
 namespace fa2 {
 
-// Wait-site ids of bad values found on the device (reported with FA2_ERR_INVALID_ARG).
-enum PagedSite : uint32_t { kPSiteBlock = 120, kPSiteSlot = 121 };
-constexpr unsigned int kStatusInvalid = 1u;
-
 // ------------------------------------------------------------------------------------
 // tables
 // ------------------------------------------------------------------------------------

@@ -12,7 +12,7 @@
 #include "fa2_host.h"
 #include "fa2_paged.cuh"
 #include "fa2_seq_bwd.cuh"
-#include "fa2_seq_fwd.cuh"
+#include "fa2_seq_host.h"
 
 namespace {
 
@@ -52,77 +52,9 @@ bool cache_ok(const fa2_cache* x, int blocks, int heads, int rows, int d) {
 
 // Sequences that may hold a partial block: the empty ones too where the order of the blocks
 // keeps a place for each (BlockOrder).
-int partial_blocks(int B, int T) { return B > fa2::kHeld ? B : std::min(B, T); }
+int partial_blocks(int B, int T, int held) { return B > held ? B : std::min(B, T); }
 
 // ---- forward over packed sequences and paged caches ----
-
-int fwd_tile_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
-
-constexpr int kDevices = 64;
-
-template <typename Kern>
-bool set_smem_once(Kern kern, int dev, int smem, std::atomic<bool> (&done)[kDevices]) {
-  if (dev < 0 || dev >= kDevices) return false;
-  if (done[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  done[dev].store(true, std::memory_order_release);
-  return true;
-}
-
-struct SeqMaps {
-  CUtensorMap q, k, v;
-};
-
-template <int D, bool BF16, int QT>
-int launch_seq(const SeqMaps& m, const fa2::SeqParams& p, int dev, unsigned int grid, cudaStream_t stream) {
-  using Cfg = fa2::SeqCfg<D, QT>;
-  auto kern = fa2::fa2_seq_fwd_kernel<D, BF16, QT>;
-  // The kernel re-splits its registers between warpgroups: only sound when every thread
-  // was launched with exactly LAUNCH_REGS of them.
-  static const bool regs_ok = [&] {
-    cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs == Cfg::LAUNCH_REGS;
-  }();
-  static std::atomic<bool> smem_set[kDevices];
-  if (!regs_ok || !set_smem_once(kern, dev, Cfg::SMEM, smem_set)) {
-    cudaGetLastError();
-    return FA2_ERR_CUDA;
-  }
-  kern<<<grid, Cfg::THREADS, Cfg::SMEM, stream>>>(m.q, m.k, m.v, p);
-  if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
-  fa2::host_count_launches(1);
-  if (!p.block_table || grid < 2) return FA2_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, QT == 1 ? 2 : 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa2::fa2_seq_merge_kernel<D, BF16, QT>, p, static_cast<int>(grid)) != cudaSuccess) {
-    cudaGetLastError();
-    return FA2_ERR_CUDA;
-  }
-  fa2::host_count_launches(1);
-  return FA2_OK;
-}
-
-int launch_seq_any(int d, bool bf, int qt, const SeqMaps& m, const fa2::SeqParams& p, int dev, unsigned int grid,
-                   cudaStream_t s) {
-#define FA2_SEQ(D_, QT_) return bf ? launch_seq<D_, true, QT_>(m, p, dev, grid, s) : launch_seq<D_, false, QT_>(m, p, dev, grid, s)
-  switch (fwd_tile_dim(d)) {
-    case 64: if (qt == 2) { FA2_SEQ(64, 2); } FA2_SEQ(64, 1);
-    case 128: if (qt == 2) { FA2_SEQ(128, 2); } FA2_SEQ(128, 1);
-    case 192: FA2_SEQ(192, 1);
-    default: FA2_SEQ(256, 1);
-  }
-#undef FA2_SEQ
-}
 
 // [T][heads][d] as a 3-D map (column, head, row) or (column, row, head).  The stride of
 // an axis with one entry is not the caller's.
@@ -176,7 +108,7 @@ int paged_tiles(int B, int T, int G, int d) { return d <= 128 && T > static_cast
 
 // Float partials of the shares: two slots each, O then LSE.
 size_t paged_opart_bytes(int grid, int qt, int d) {
-  return static_cast<size_t>(grid) * 2 * qt * 128 * fwd_tile_dim(d) * 4;
+  return static_cast<size_t>(grid) * 2 * qt * 128 * fa2::seq_tile_dim(d) * 4;
 }
 size_t paged_bytes(int grid, int qt, int d) {
   return paged_opart_bytes(grid, qt, d) + static_cast<size_t>(grid) * 2 * qt * 128 * 4;
@@ -220,8 +152,8 @@ template <int D, bool BF16>
 int launch_seq_bwd(const CUtensorMap (&m)[5], const fa2::SeqBwdParams& p, int dev, unsigned int items, cudaStream_t s) {
   using Cfg = fa2::SeqBwdCfg<D>;
   auto kern = fa2::fa2_seq_bwd_kernel<D, BF16>;
-  static std::atomic<bool> smem_set[kDevices];
-  if (!set_smem_once(kern, dev, Cfg::SMEM, smem_set)) return FA2_ERR_CUDA;
+  static std::atomic<bool> smem_set[fa2::kSeqDevices];
+  if (!fa2::seq_smem_once(kern, dev, Cfg::SMEM, smem_set)) return FA2_ERR_CUDA;
   const dim3 rows(static_cast<unsigned int>(p.tiles) * (128 * D / 8 / 256), p.Hkv);
   if (!launch_chained(fa2::fa2_seq_bwd_pre_kernel<D, BF16>, rows, 256, 0, s, p) ||
       !launch_chained(kern, dim3(items), Cfg::THREADS, Cfg::SMEM, s, m[0], m[1], m[2], m[3], m[4], p) ||
@@ -254,20 +186,20 @@ int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   const int G = H / Hkv, tpt = 128 / G;
   // Items there could be: every sequence's last block may be partial.
   const auto items = [&](int qt) {
-    return (static_cast<long long>(T) / (qt * tpt) + partial_blocks(B, T)) * Hkv;
+    return (static_cast<long long>(T) / (qt * tpt) + partial_blocks(B, T, fa2::kHeld)) * Hkv;
   };
   // Two query tiles to a CTA; one (twice the CTAs) where two would leave SMs without work.
   const int qt = d <= 128 && items(2) >= n_sm ? 2 : 1;
   if (items(qt) > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
-  SeqMaps m;
+  fa2::SeqMaps m;
   if (!map_packed(&m.q, Q, T, H, d, dtype, false, tpt, G) || !map_packed(&m.k, K, T, Hkv, d, dtype, true, 128, 1) ||
       !map_packed(&m.v, V, T, Hkv, d, dtype, true, 128, 1))
     return FA2_ERR_CUDA;
   fa2::SeqParams p = seq_params(O, LSE, cu_seqlens, st, B, T, H, Hkv, d, scale, causal, window);
   const long long per_head = items(qt) / Hkv;
   p.head_group = static_cast<int>(std::min<long long>(Hkv, std::max<long long>(1, (2LL * n_sm + per_head - 1) / per_head)));
-  return launch_seq_any(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(items(qt)),
-                        reinterpret_cast<cudaStream_t>(stream));
+  return fa2::launch_seq_packed(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(items(qt)),
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t fa2_bwd_varlen_workspace_size(int B, int T, int H, int Hkv, int d) {
@@ -304,7 +236,7 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   if (rc != FA2_OK) return rc;
   const int G = H / Hkv, tpt = 128 / G, D = bwd_tile_dim(d);
   const long long tiles = bwd_tiles(B, T, G);
-  const long long items = (T / 128 + static_cast<long long>(partial_blocks(B, T))) * Hkv;
+  const long long items = (T / 128 + static_cast<long long>(partial_blocks(B, T, fa2::kHeldBwd))) * Hkv;
   if (tiles * 128 > 0x7fffffffll || items > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t stat = bwd_stat_bytes(B, T, H, Hkv);
@@ -392,7 +324,7 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
       workspace_bytes < fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, n_sm))
     return FA2_ERR_WORKSPACE;
   const int G = H / Hkv, qt = paged_tiles(B, T, G, d);
-  SeqMaps m;
+  fa2::SeqMaps m;
   if (!map_packed(&m.q, Q, T, H, d, dtype, false, 128 / G, G) ||
       !map_cache(&m.k, K, num_blocks, Hkv, block_size, d, dtype) ||
       !map_cache(&m.v, V, num_blocks, Hkv, block_size, d, dtype))
@@ -404,8 +336,8 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
   p.box_rows = std::min(block_size, 128);
   p.O_part = static_cast<float*>(workspace);
   p.LSE_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_opart_bytes(n_sm, qt, d));
-  return launch_seq_any(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(n_sm),
-                        reinterpret_cast<cudaStream_t>(stream));
+  return fa2::launch_seq_paged(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(n_sm),
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 int fa2_paged_tables(const int* context_lens, const int* new_lens, const int* free_blocks,

@@ -154,6 +154,8 @@ struct SeqBwdCfg {
   __host__ __device__ static constexpr uint32_t C_DS(int g) { return D == 128 ? 64u * g + 32u : C_DP + 64u * g; }
 };
 
+constexpr int kHeldBwd = 96;  // as kHeld; what shared memory has left at D = 128
+
 struct SeqBwdCtrl {
   uint4 clc_response;
   SeqBwdItem items[kSeqItems];
@@ -163,6 +165,7 @@ struct SeqBwdCtrl {
   uint64_t s_full, dp_full, p_ready, ds_ready, dq_full, dq_drained, drain, fin;
   uint32_t tmem_slot;
   int abort_flag;
+  int held[kHeldBwd];  // the scheduling warp's
 };
 
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gmem_src, uint32_t bytes, uint64_t* bar) {
@@ -265,8 +268,8 @@ fa2_seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       ++ii;
       return true;
     };
-    BlockOrder order;
-    order.load(p.cu, p.B, p.T, 128, lane);
+    BlockOrder<kHeldBwd> order;
+    order.load(ctl.held, p.cu, p.B, p.T, 128, lane);
     int w = blockIdx.x;
     BlockAt at;
     for (int k = 0; ok && w >= 0; ++k) {

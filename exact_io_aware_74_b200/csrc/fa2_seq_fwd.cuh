@@ -34,7 +34,6 @@
 
 #include <cstdint>
 
-#include "fa2_paged.cuh"
 #include "ptx.cuh"
 
 namespace fa2 {
@@ -45,7 +44,7 @@ struct SeqParams {
   float* LSE;               // [H][T]
   const int* cu;            // [B + 1]
   const int* seq_lens;      // paged: [B]
-  const int* block_table;   // paged: [B][max_blocks]; nullptr: packed keys
+  const int* block_table;   // paged: [B][max_blocks]
   float* O_part;            // [2 grid][QT * 128][D]
   float* LSE_part;          // [2 grid][QT * 128]
   unsigned int* status;
@@ -87,7 +86,7 @@ enum SeqSite : uint32_t {
 };
 
 constexpr int kSeqItems = 4;  // ring of items handed to the roles
-constexpr int kHeld = 256;    // sequences whose lengths a scheduling warp holds in registers
+constexpr int kHeld = 256;    // sequences whose counts a scheduling warp keeps in shared memory
 
 struct SeqItem {
   int row0, n_tok;   // first packed query row, tokens
@@ -110,12 +109,13 @@ struct SeqLen {
   int row0, n, nk;
 };
 
+template <bool PAGED>
 __device__ __forceinline__ SeqLen seq_len(const SeqParams& p, int b) {
   SeqLen s;
   s.row0 = min(max(p.cu[b], 0), p.T);
   s.n = min(max(p.cu[b + 1], s.row0), p.T) - s.row0;
   s.nk = s.n;
-  if (p.block_table) s.nk = min(max(p.seq_lens[b], 0), p.max_blocks * p.block_size);
+  if (PAGED) s.nk = min(max(p.seq_lens[b], 0), p.max_blocks * p.block_size);
   return s;
 }
 
@@ -130,13 +130,13 @@ __device__ __forceinline__ void key_range(const SeqParams& p, const SeqLen& s, i
   if (hi <= lo) lo = hi = 0;
 }
 
-template <int QT>
+template <bool PAGED, int QT>
 __device__ __forceinline__ void make_item(const SeqParams& p, const SeqLen& s, int b, int kvh, int blk, SeqItem& it) {
   const int a = blk * (QT * p.tpt), e = min(s.n, a + QT * p.tpt), m = min(e, a + p.tpt);
   it.row0 = s.row0 + a;
   it.n_tok = e - a;
   it.kvh = kvh;
-  it.key0 = p.block_table ? b : s.row0;
+  it.key0 = PAGED ? b : s.row0;
   it.nk = s.nk;
   it.pos = s.nk - s.n + a;
   it.first = p.window > 0 ? max(0, it.pos - p.window + 1) : 0;
@@ -213,131 +213,119 @@ __device__ __forceinline__ int share_ctas(long long units, int grid) {
 }
 __device__ __forceinline__ long long share_start(long long units, int ctas, int c) { return units * c / ctas; }
 
-// The linear order of the units: sequence, head, block, key tile.  Whole warp; up to kHeld
-// sequences' units stay in registers between the total and the search.
+// The linear order of the units: sequence, head, block, key tile.  Whole warp.
 struct UnitAt {
   int b, kvh, blk, at;  // at: units of the block before x
   SeqLen s;
 };
-template <int QT>
-struct UnitOrder {
-  int u[kHeld / 32];
-  long long total;  // of all heads
 
-  __device__ __forceinline__ int chunk(const SeqParams& p, int b0, int lane) const {
-    SeqLen s{0, 0, 0};
-    if (b0 + lane < p.B) s = seq_len(p, b0 + lane);
-    return lane_units<QT>(p, s.n, s.nk, lane);
-  }
-  __device__ __forceinline__ void load(const SeqParams& p, int lane) {
-    total = 0;
-    if (p.B > kHeld) {
-      for (int b0 = 0; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, chunk(p, b0, lane));
-    } else {
-      int n[kHeld / 32], nk[kHeld / 32];  // all loads before the first use
-#pragma unroll
-      for (int i = 0; i < kHeld / 32; ++i) {
+// Cuts the units of all items into shares, at most `grid` of them, and finds where share
+// `c` starts: false when there is no such share.  x, xe: its units; `held`: kHeld ints of
+// shared memory (or nullptr: the units are computed twice).  One loop body serves the
+// total and the search: this code runs once a CTA, and the instruction cache is better
+// left to the loops that run on.
+template <int QT>
+__device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, int* held, int lane, int& ctas,
+                                           long long& total, long long& x, long long& xe, UnitAt& r) {
+  total = 0;
+  int units = 1;  // of one head of the sequence found
+  long long rem = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      int v;
+      if (pass == 1 && held && b0 < kHeld) {
+        v = held[b0 + lane];
+      } else {
         SeqLen s{0, 0, 0};
-        if (i * 32 + lane < p.B) s = seq_len(p, i * 32 + lane);
-        n[i] = s.n, nk[i] = s.nk;
+        if (b0 + lane < p.B) s = seq_len<true>(p, b0 + lane);
+        v = lane_units<QT>(p, s.n, s.nk, lane);
+        if (pass == 0 && held && b0 < kHeld) held[b0 + lane] = v;
       }
-#pragma unroll
-      for (int i = 0; i < kHeld / 32; ++i) {
-        u[i] = i * 32 < p.B ? lane_units<QT>(p, n[i], nk[i], lane) : 0;
-        total += __reduce_add_sync(0xffffffffu, u[i]);
-      }
-    }
-    total *= p.Hkv;
-  }
-  // Unit x < total.
-  __device__ __forceinline__ UnitAt find(const SeqParams& p, long long x, int lane) const {
-    UnitAt r{};
-    int units = 1;  // of one head of the sequence
-    bool found = false;
-    auto look = [&](int b0, int v) {
       const int inc = warp_inclusive(v, lane);
       const long long end = static_cast<long long>(inc) * p.Hkv;
-      const unsigned int m = __ballot_sync(0xffffffffu, end > x);
+      if (pass == 0) {
+        total += __shfl_sync(0xffffffffu, end, 31);
+        continue;
+      }
+      const unsigned int m = __ballot_sync(0xffffffffu, end > rem);
       if (m) {
         const int l = __ffs(m) - 1;
         r.b = b0 + l;
         units = __shfl_sync(0xffffffffu, v, l);
-        x -= __shfl_sync(0xffffffffu, end, l) - static_cast<long long>(units) * p.Hkv;
-        found = true;
-      } else {
-        x -= __shfl_sync(0xffffffffu, end, 31);
-      }
-    };
-    if (p.B > kHeld) {
-      for (int b0 = 0; b0 < p.B && !found; b0 += 32) look(b0, chunk(p, b0, lane));
-    } else {
-#pragma unroll
-      for (int i = 0; i < kHeld / 32; ++i)
-        if (!found && i * 32 < p.B) look(i * 32, u[i]);
-    }
-    r.s = seq_len(p, r.b);
-    r.kvh = static_cast<int>(x / units);
-    int rem = static_cast<int>(x - static_cast<long long>(r.kvh) * units);
-    const int R = QT * p.tpt, nb = (r.s.n + R - 1) / R;
-    for (int i0 = 0; i0 < nb; i0 += 32) {
-      const int v = i0 + lane < nb ? block_units<QT>(p, r.s, i0 + lane) : 0;
-      const int inc = warp_inclusive(v, lane);
-      const unsigned int m = __ballot_sync(0xffffffffu, inc > rem);
-      if (m) {
-        const int l = __ffs(m) - 1;
-        r.blk = i0 + l;
-        rem -= __shfl_sync(0xffffffffu, inc - v, l);
+        rem -= __shfl_sync(0xffffffffu, end, l) - static_cast<long long>(units) * p.Hkv;
         break;
       }
-      rem -= __shfl_sync(0xffffffffu, inc, 31);
+      rem -= __shfl_sync(0xffffffffu, end, 31);
     }
-    r.at = rem;
-    return r;
+    if (pass == 0) {
+      ctas = share_ctas(total, grid);
+      if (c >= ctas || total == 0) return false;
+      x = rem = share_start(total, ctas, c);
+      xe = share_start(total, ctas, c + 1);
+      __syncwarp();
+    }
   }
-};
+  r.s = seq_len<true>(p, r.b);
+  r.kvh = static_cast<int>(rem / units);
+  int at = static_cast<int>(rem - static_cast<long long>(r.kvh) * units);
+  const int R = QT * p.tpt, nb = (r.s.n + R - 1) / R;
+  r.blk = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < nb; i0 += 32) {
+    const int v = i0 + lane < nb ? block_units<QT>(p, r.s, i0 + lane) : 0;
+    const int inc = warp_inclusive(v, lane);
+    const unsigned int m = __ballot_sync(0xffffffffu, inc > at);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      r.blk = i0 + l;
+      at -= __shfl_sync(0xffffffffu, inc - v, l);
+      break;
+    }
+    at -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  r.at = at;
+  return true;
+}
 
 __device__ __forceinline__ int rows_of(const int* cu, int T, int b) {
   const int s = min(max(cu[b], 0), T);
   return min(max(cu[b + 1], s), T) - s;
 }
 
-// Packed: the order of the items, found by one warp.  Up to kHeld sequences their block
-// counts sit in registers, and the order is head group by head group, in a group the
-// blocks of the highest level (index from the sequence's start) of all sequences first,
+// Packed: the order of the items, found by one warp.  Up to CAP sequences their block
+// counts are kept in shared memory, and the order is head group by head group, in a group
+// the blocks of the highest level (index from the sequence's start) of all sequences first,
 // heads innermost: heaviest first, when causal.  With more sequences the blocks lie
 // sequence by sequence, highest first (cu[b] / R + b is where sequence b's start: its last
-// block may be partial, so some places hold none).  Searching the counts in memory for the
-// first order took 5 to 9 us an item with 148 and 740 sequences (B200); either of these
-// takes well under 1.
+// block may be partial, so some places hold none).  Searching the counts in global memory
+// for the first order took 5 to 9 us an item with 148 and 740 sequences (B200).
 struct BlockAt {
   int b, level, kvh;
 };
 
+template <int CAP>  // sequences whose counts fit
 struct BlockOrder {
-  int nb[kHeld / 32];   // blocks of sequences lane, lane + 32, ...
+  int* held;
   int n_blocks, max_blk;  // of one head; of one sequence
 
-  __device__ __forceinline__ void load(const int* cu, int B, int T, int R, int lane) {
-    if (B > kHeld) {
-      n_blocks = T / R + B;
-      return;
-    }
+  __device__ __forceinline__ void load(int* shared, const int* cu, int B, int T, int R, int lane) {
+    held = shared;
+    max_blk = 0;
+    n_blocks = T / R + B;
+    if (B > CAP) return;
     int sum = 0, most = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld / 32; ++i) {
-      const int b = i * 32 + lane;
-      nb[i] = b < B ? (rows_of(cu, T, b) + R - 1) / R : 0;
-      sum += nb[i];
-      most = max(most, nb[i]);
+#pragma unroll 2
+    for (int b = lane; b < B; b += 32) {
+      const int n = (rows_of(cu, T, b) + R - 1) / R;
+      held[b] = n;
+      sum += n;
+      most = max(most, n);
     }
     n_blocks = __reduce_add_sync(0xffffffffu, sum);
     max_blk = __reduce_max_sync(0xffffffffu, most);
-  }
-  __device__ __forceinline__ int from(int level) const {  // blocks of that level and above
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld / 32; ++i) c += max(0, nb[i] - level);
-    return __reduce_add_sync(0xffffffffu, c);
+    __syncwarp();
   }
   // Item w (whole warp); false when the place holds none.
   __device__ __forceinline__ bool find(const int* cu, int B, int T, int Hkv, int head_group, int R, int w, int lane,
@@ -347,8 +335,9 @@ struct BlockOrder {
     const int heads = min(head_group, Hkv - grp * head_group);
     const int rank = at / heads;
     r.kvh = grp * head_group + at - rank * heads;
-    if (B > kHeld) {
+    if (B > CAP) {
       int lo = 0, n = B;  // the last sequence whose place is at or before rank is in [lo, lo + n)
+#pragma unroll 1
       while (n > 1) {
         const int step = (n + 31) / 32, b = lo + lane * step;
         const bool le = lane * step < n && min(max(cu[b], 0), T) / R + b <= rank;
@@ -361,23 +350,32 @@ struct BlockOrder {
       r.level = blocks - 1 - (rank - (min(max(cu[lo], 0), T) / R + lo));
       return r.level >= 0 && r.level < blocks;
     }
-    int lo = 0, hi = max_blk;  // the largest level with from(level) > rank
+    // The largest level with more than `rank` blocks at that level and above, by bisection;
+    // `above`: the blocks above it.
+    int lo = 0, hi = max_blk, above = 0;
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (from(mid) > rank) lo = mid; else hi = mid;
+      int c = 0;
+#pragma unroll 2
+      for (int b = lane; b < B; b += 32) c += max(0, held[b] - mid);
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c > rank) lo = mid; else hi = mid, above = c;
     }
     r.level = lo;
-    int i = rank - from(lo + 1);  // the i-th sequence with more than lo blocks
-    r.b = -1;
-#pragma unroll
-    for (int c = 0; c < kHeld / 32; ++c) {
-      const bool has = nb[c] > lo;
+    int i = rank - above;  // the i-th sequence with more than lo blocks
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const bool has = b0 + lane < B && held[b0 + lane] > lo;
       const unsigned int m = __ballot_sync(0xffffffffu, has);
       const unsigned int hit = __ballot_sync(0xffffffffu, has && __popc(m & ((1u << lane) - 1u)) == i);
-      if (r.b < 0 && hit) r.b = c * 32 + __ffs(hit) - 1;
+      if (hit) {
+        r.b = b0 + __ffs(hit) - 1;
+        return true;
+      }
       i -= __popc(m);
     }
-    return r.b >= 0;
+    return false;
   }
 };
 
@@ -423,13 +421,45 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
 // the kernel
 // ------------------------------------------------------------------------------------
 
+// mbar_wait with its loop out of line, for the roles off the critical path (with it in the
+// MMA issuer the not causal 2 x 32 x 8192 forward took 2590 us, not 2250): some thirty
+// copies of the loop are a quarter of the kernel's code, and what runs once an item then
+// misses the instruction cache (238 KB of code ran items of one key tile at 11 us, 127 KB at
+// 7 us; B200).
+static __device__ __noinline__ bool mbar_wait_loop(uint32_t bar, uint32_t parity, unsigned int* status,
+                                                   volatile int* abort, uint64_t limit_ns, uint32_t site) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 15u) == 0u) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > limit_ns) {
+        report_timeout(WaitCtl{status, abort, limit_ns}, site);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity, const WaitCtl& w, uint32_t site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_loop(smem_u32(bar), parity, w.status, w.abort, w.limit_ns, site);
+}
+
 // Keys of tile j that some row of the item sees, counted from the tile's first key.
 __device__ __forceinline__ void tile_keys(const SeqItem& it, int j, int& a, int& e) {
   a = max(it.first - j * 128, 0);
   e = min(it.nk - j * 128, 128);
 }
 
-template <int D, bool BF16, int QT>
+template <int D, bool BF16, int QT, bool PAGED>
 __global__ void __launch_bounds__(384, 1)
 fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const SeqParams p) {
@@ -450,12 +480,12 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __shared__ uint64_t s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int held[kHeld];  // the scheduling warp's
 
   griddep_launch_dependents();  // the merge kernel waits for this grid before it reads
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const bool paged = p.block_table != nullptr;
   WaitCtl wc{p.status, &abort_flag, p.wait_ns};
 
   if (threadIdx.x == 8 * 32) {
@@ -502,7 +532,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       auto publish = [&](const SeqItem& it) -> bool {
         const int s = ii % NI;
         bool ok = true;
-        if (ii >= NI) ok = mbar_wait(&item_empty[s], ((ii / NI) - 1) & 1, wc, kQSiteItemEmpty);
+        if (ii >= NI) ok = mbar_wait_far(&item_empty[s], ((ii / NI) - 1) & 1, wc, kQSiteItemEmpty);
         if (!__all_sync(0xffffffffu, ok)) return false;
         if (lane == 0) {
           items[s] = it;
@@ -513,20 +543,18 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       };
       SeqItem it{};
       bool ok = true;
-      if (paged) {
-        UnitOrder<QT> order;
-        order.load(p, lane);
-        const long long units = order.total;
-        const int ctas = share_ctas(units, gridDim.x), c = blockIdx.x;
-        long long x = share_start(units, ctas, c);
-        const long long xe = c < ctas ? share_start(units, ctas, c + 1) : x;
-        if (x < xe) {
-          UnitAt u = order.find(p, x, lane);
+      if constexpr (PAGED) {
+        const int c = blockIdx.x;
+        int ctas;
+        long long units, x, xe;
+        UnitAt u;
+        if (find_share<QT>(p, gridDim.x, c, held, lane, ctas, units, x, xe, u) && x < xe) {
           const int R = QT * p.tpt;
+#pragma unroll 1
           while (ok) {
             const int len = block_units<QT>(p, u.s, u.blk);
             const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
-            make_item<QT>(p, u.s, u.b, u.kvh, u.blk, it);
+            make_item<true, QT>(p, u.s, u.b, u.kvh, u.blk, it);
             if (u.at > 0 || take < len) {
               cut_item(it, u.at, u.at + take);
               it.part = 2 * c + (u.at > 0 ? 0 : 1);
@@ -539,26 +567,26 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               u.blk = 0;
               if (++u.kvh >= p.Hkv) {
                 u.kvh = 0;
-                do u.s = seq_len(p, ++u.b); while (u.s.n == 0 && u.b + 1 < p.B);  // units are left
+                do u.s = seq_len<true>(p, ++u.b); while (u.s.n == 0 && u.b + 1 < p.B);  // units are left
               }
             }
           }
         }
       } else {
         const int R = QT * p.tpt;
-        BlockOrder order;
-        order.load(p.cu, p.B, p.T, R, lane);
+        BlockOrder<kHeld> order;
+        order.load(held, p.cu, p.B, p.T, R, lane);
         BlockAt at;
         int w = blockIdx.x;
         for (int k = 0; ok && w >= 0; ++k) {
           if (order.find(p.cu, p.B, p.T, p.Hkv, p.head_group, R, w, lane, at)) {
-            make_item<QT>(p, seq_len(p, at.b), at.b, at.kvh, at.level, it);
+            make_item<false, QT>(p, seq_len<false>(p, at.b), at.b, at.kvh, at.level, it);
             ok = publish(it);
           }
           // The next index only once the item before this one is done with: a CTA holds
           // at most one item that it has not begun.
           if (ok && ii >= 2)
-            ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[(ii - 2) % NI], ((ii - 2) / NI) & 1, wc, kQSiteItemEmpty));
+            ok = __all_sync(0xffffffffu, mbar_wait_far(&item_empty[(ii - 2) % NI], ((ii - 2) / NI) & 1, wc, kQSiteItemEmpty));
           if (!ok) break;
           if (lane == 0) {
             fence_proxy_async_smem();  // the response was read before it is written again
@@ -568,7 +596,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           __syncwarp();
           volatile int no_abort = 0;  // the response always lands before the CTA leaves
           WaitCtl cw{p.status, &no_abort, p.wait_ns};
-          ok = __all_sync(0xffffffffu, mbar_wait(&clc_full, k & 1, cw, kQSiteClc));
+          ok = __all_sync(0xffffffffu, mbar_wait_far(&clc_full, k & 1, cw, kQSiteClc));
           if (!ok) break;
           w = lane == 0 ? clc_index(&clc_response) : 0;
           w = __shfl_sync(0xffffffffu, w, 0);
@@ -583,9 +611,9 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       unsigned int raw = 0;             // V slots whose last load went to v_raw
       unsigned int raw_par = 0;         // parity of the loads on v_raw, per slot
       bool ok = true, skipped = false;  // test hook: the first K tile was not loaded
-      const int nbox = 128 / (paged ? p.box_rows : 128);
+      const int nbox = 128 / (PAGED ? p.box_rows : 128);
       auto wait_all = [&](uint64_t* bar, uint32_t par) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, par, wc, kQSiteProd)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_far(bar, par, wc, kQSiteProd)) != 0;
       };
       auto load_q = [&](const SeqItem& it, int t) -> bool {
         const int s = qc % C::QS;
@@ -613,25 +641,25 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         return pg;
       };
       auto load_tile = [&](const SeqItem& it, int j, int pg, const CUtensorMap* map, uint8_t* dst, uint64_t* bar) {
-        if (!paged) {
+        if constexpr (!PAGED) {
           if (lane == 0) {
             mbar_arrive_expect_tx(bar, C::TILE);
             for (int c = 0; c < C::KCH; ++c)
               tma_load_3d_hint(dst + c * C::CHUNK, map, bar, c * 64, it.key0 + j * 128, it.kvh, keep);
           }
-          return;
-        }
-        int a, e;
-        tile_keys(it, j, a, e);
-        const int i0 = a / p.box_rows, n = (e + p.box_rows - 1) / p.box_rows - i0;
-        if (lane == 0) mbar_arrive_expect_tx(bar, n * p.box_rows * 128 * C::KCH);
-        __syncwarp();
-        for (int x0 = 0; x0 < n * C::KCH; x0 += 32) {
-          const int x = x0 + lane, i = i0 + x / C::KCH, c = x % C::KCH;
-          const int page = __shfl_sync(0xffffffffu, pg, i & 31);
-          if (x < n * C::KCH)
-            tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64,
-                        (j * 128 + i * p.box_rows) % p.block_size, it.kvh, page);
+        } else {
+          int a, e;
+          tile_keys(it, j, a, e);
+          const int i0 = a / p.box_rows, n = (e + p.box_rows - 1) / p.box_rows - i0;
+          if (lane == 0) mbar_arrive_expect_tx(bar, n * p.box_rows * 128 * C::KCH);
+          __syncwarp();
+          for (int x0 = 0; x0 < n * C::KCH; x0 += 32) {
+            const int x = x0 + lane, i = i0 + x / C::KCH, c = x % C::KCH;
+            const int page = __shfl_sync(0xffffffffu, pg, i & 31);
+            if (x < n * C::KCH)
+              tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64,
+                          (j * 128 + i * p.box_rows) % p.block_size, it.kvh, page);
+          }
         }
       };
       auto load_k = [&](const SeqItem& it, int j, int pg) -> bool {
@@ -663,11 +691,11 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (lane == 0) mbar_arrive(&item_empty[ii % NI]);
         if (!it.valid) break;
         if (it.n == 0) continue;
-        int pg = paged ? pages_of(it, it.j0) : 0;
+        int pg = PAGED ? pages_of(it, it.j0) : 0;
         if (it.hi[0] > 0) ok = load_q(it, 0);
         for (int jj = 0; jj < it.n && ok; ++jj) {
           const int j = it.j0 + jj;
-          const int pg_next = paged && jj + 1 < it.n ? pages_of(it, j + 1) : 0;
+          const int pg_next = PAGED && jj + 1 < it.n ? pages_of(it, j + 1) : 0;
           ok = load_k(it, j, pg);
           if (QT == 2) {
             if (ok && jj == 0 && it.hi[1] > 0) ok = load_q(it, 1);
@@ -686,13 +714,13 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // Every copy that was issued lands before the CTA leaves, on a timeout too.
         volatile int no_abort = 0;
         WaitCtl dw{p.status, &no_abort, 100000000ull};
-        for (int i = max(0, qc - C::QS); i < qc; ++i) mbar_wait(&q_full[i % C::QS], (i / C::QS) & 1, dw, kQSiteDrain);
+        for (int i = max(0, qc - C::QS); i < qc; ++i) mbar_wait_far(&q_full[i % C::QS], (i / C::QS) & 1, dw, kQSiteDrain);
         for (int i = max(0, kc - C::KS); i < kc; ++i)
-          if (!(skipped && i == 0)) mbar_wait(&k_full[i % C::KS], (i / C::KS) & 1, dw, kQSiteDrain);
+          if (!(skipped && i == 0)) mbar_wait_far(&k_full[i % C::KS], (i / C::KS) & 1, dw, kQSiteDrain);
         for (int i = max(0, vc - C::VS); i < vc; ++i) {
           const int s = i % C::VS;
-          if (raw >> s & 1) mbar_wait(&v_raw[s], (raw_par >> s & 1) ^ 1, dw, kQSiteDrain);
-          else mbar_wait(&v_full[s], (i / C::VS) & 1, dw, kQSiteDrain);
+          if (raw >> s & 1) mbar_wait_far(&v_raw[s], (raw_par >> s & 1) ^ 1, dw, kQSiteDrain);
+          else mbar_wait_far(&v_full[s], (i / C::VS) & 1, dw, kQSiteDrain);
         }
       }
       __syncwarp();
@@ -702,7 +730,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       unsigned int par = 0;
       bool ok = true;
       for (int ii = 0; ok; ++ii) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem));
+        ok = __all_sync(0xffffffffu, mbar_wait_far(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem));
         if (!ok) break;
         const SeqItem it = items[ii % NI];
         __syncwarp();
@@ -713,7 +741,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           tile_keys(it, it.j0 + jj, a, e);
           if (a <= 0 && e >= 128) continue;
           const int s = vc % C::VS;
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_raw[s], par >> s & 1, wc, kQSiteFix));
+          ok = __all_sync(0xffffffffu, mbar_wait_far(&v_raw[s], par >> s & 1, wc, kQSiteFix));
           if (!ok) break;
           par ^= 1u << s;
           uint8_t* v = sV + s * C::TILE + (lane & 7) * 16;
@@ -1028,7 +1056,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // A row that sees no key: O = 0, LSE = -inf.
       const float inv_l = (l > 0.f && lr > 0.f) ? 1.0f / lr : 0.f;
       const float lse = (l > 0.f) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-      const int part = it.part;
+      const int part = PAGED ? it.part : -1;  // packed items are never cut
       if (live) {
         const int row = it.row0 + tok, head = it.kvh * G + g_r;
         uint16_t* orow = p.O + row * p.o_row + head * p.o_head;
@@ -1098,13 +1126,11 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 template <int D, bool BF16, int QT>
 __global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p, int grid) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  UnitOrder<QT> order;
-  order.load(p, lane);
-  const long long units = order.total;
-  const int ctas = share_ctas(units, grid), c = blockIdx.x + 1;
-  if (c >= ctas || units == 0) return;
-  const long long x = share_start(units, ctas, c);
-  const UnitAt u = order.find(p, x, lane);
+  const int c = blockIdx.x + 1;
+  int ctas;
+  long long units, x, xe;
+  UnitAt u;
+  if (!find_share<QT>(p, grid, c, nullptr, lane, ctas, units, x, xe, u)) return;
   if (u.at == 0 || share_start(units, ctas, c - 1) > x - u.at) return;
   const long long end = x - u.at + block_units<QT>(p, u.s, u.blk);
   int last = c;  // the last share with a part of the block

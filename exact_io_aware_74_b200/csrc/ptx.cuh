@@ -98,6 +98,9 @@ struct WaitCtl {
 
 // Device status word layout: low 8 bits = status code, bits 8..15 = wait site.
 constexpr unsigned int kStatusTimeout = 5u;
+// Bad values found on the device (a block or slot outside the cache), and their sites.
+constexpr unsigned int kStatusInvalid = 1u;
+constexpr uint32_t kPSiteBlock = 120, kPSiteSlot = 121;
 
 static __device__ __noinline__ void report_timeout(const WaitCtl& w, uint32_t site) {
   *w.abort = 1;

@@ -119,7 +119,7 @@ def test_many_requests():
     n = 300
     Step([r.randrange(400) for _ in range(n)], [r.choice([0, 1, 1, 1, 2]) for _ in range(n)], 4, 1, 64, 16, "bf16",
          seed=4).check()
-    for n in (256, 257, 600):  # about as many as a scheduling warp holds in registers
+    for n in (256, 257, 600):  # about as many as a scheduling warp keeps the counts of
         new = [r.choice([0, 1, 5]) for _ in range(n)]
         new[n // 2] = 200
         Step([r.randrange(60) for _ in range(n)], new, 4, 2, 64, 16, "bf16", seed=n).check()

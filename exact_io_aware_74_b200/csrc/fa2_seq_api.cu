@@ -401,10 +401,11 @@ int fa2_paged_append(const fa2_packed* K, const fa2_packed* V, const fa2_cache* 
   p.slots = slots;
   p.status = st;
   p.T = T, p.Hkv = Hkv, p.vec = d / 8, p.num_blocks = num_blocks, p.block_size = block_size;
-  const long long n = static_cast<long long>(T) * Hkv * p.vec;
-  if ((n + 255) / 256 > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
-  const dim3 grid(static_cast<unsigned int>((n + 255) / 256), 2);
-  fa2::fa2_paged_append_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const int row = Hkv * p.vec, tx = std::min(row, fa2::kAppendThreads), ty = fa2::kAppendThreads / tx;
+  const int per = fa2::kAppendRows * ty, pieces = (row + tx - 1) / tx;
+  if (pieces > 32767) return FA2_ERR_INVALID_ARG;
+  const dim3 grid((T + per - 1) / per, 2 * pieces);
+  fa2::fa2_paged_append_kernel<<<grid, dim3(tx, ty), 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
   fa2::host_count_launches(1);
   return FA2_OK;

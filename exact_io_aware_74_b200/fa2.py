@@ -9,6 +9,7 @@ missing or unloadable library raises ``RuntimeError`` -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -273,141 +274,137 @@ def fa2_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, scale: float, causal: bool,
 # packed sequences, grouped heads and paged caches
 # ------------------------------------------------------------------------------------
 
-def _check_rows(dtype, *ts) -> None:
-    """[T, heads, d] tensors of one 16-bit dtype on one device, columns contiguous."""
-    dev = ts[0].device
-    for t in ts:
-        if t.dim() != 3 or not t.is_cuda or t.dtype != dtype or t.device != dev:
-            raise ValueError("packed tensors must be [T, heads, d] CUDA tensors of one dtype "
-                             "on one device")
-        if t.stride(2) != 1 and t.shape[2] != 1:
-            raise ValueError("the columns of a packed tensor must be contiguous")
+# These calls take few microseconds on the device for a decode step, so the checks are
+# written for the host time they cost.
+
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return dev
 
 
-def _check_ints(device, **ts) -> None:
-    for name, t in ts.items():
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-
-
-def _packed(t) -> FA2Packed:
-    row, head, _ = t.stride()
+def _rows(name: str, t, shape, dtype, dev: int) -> FA2Packed:
+    """A [T, heads, d] tensor of the given shape, dtype and device, columns contiguous."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor on cuda:{dev}, not "
+                         f"{list(t.shape)} {t.dtype} on {t.device}")
+    row, head, col = t.stride()
+    if col != 1 and shape[2] != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
     return FA2Packed(t.data_ptr(), row, head)
 
 
-def _cache(t) -> FA2Cache:
-    block, head, row, _ = t.stride()
+def _pages(name: str, t, shape, dtype, dev: int) -> FA2Cache:
+    """A [blocks, heads, block_size, d] cache, columns contiguous."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor on cuda:{dev}, not "
+                         f"{list(t.shape)} {t.dtype} on {t.device}")
+    block, head, row, col = t.stride()
+    if col != 1 and shape[3] != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
     return FA2Cache(t.data_ptr(), block, head, row)
 
 
-class _on:
-    """Makes ``device`` current for a call (the library works on the current device)."""
-    __slots__ = ("idx", "old")
-
-    def __init__(self, device):
-        self.idx = device.index
-
-    def __enter__(self):
-        self.old = torch.cuda.current_device()
-        if self.old != self.idx:
-            torch.cuda.set_device(self.idx)
-
-    def __exit__(self, *exc):
-        if self.old != self.idx:
-            torch.cuda.set_device(self.old)
+def _ints(name: str, t, n: int, dev: int) -> int:
+    """Address of a contiguous int32 tensor of n numbers."""
+    if t.dtype != torch.int32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} numbers on cuda:{dev}, "
+                         f"not {list(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
-def _check_lse(lse, H: int, T: int, device) -> None:
-    if lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous() or \
-            lse.device != device:
-        raise ValueError(f"lse must be a contiguous float32 [{H}, {T}] tensor on {device}")
+def _lse(t, H: int, T: int, dev: int) -> int:
+    if t.dtype != torch.float32 or t.shape != (H, T) or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 [{H}, {T}] tensor on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _same_shape(shape, **ts) -> None:
-    for name, t in ts.items():
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+def _dims(name: str, t, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, not {list(t.shape)}")
+    return t.shape
+
+
+def _call(fn, dev: int, stream, *args) -> int:
+    """Calls ``fn`` with the stream (of ``dev``'s current one) last, on device ``dev``: the
+    library works on the current device."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
+
+
+def _bytes(workspace, dev: int) -> tuple[int | None, int]:
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def fa2_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale: float, causal: bool, window: int = 0,
                    stream=None) -> int:
     """Raw call: q, o [T,H,d] and k, v [T,Hkv,d] 16-bit, any row and head strides that are
     multiples of 8; lse [H,T] float32; cu_seqlens [B+1] int32.  Returns the status."""
-    _check_rows(q.dtype, q, k, v, o)
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    _same_shape((T, Hkv, d), k=k, v=v)
-    _same_shape(q.shape, o=o)
-    _check_lse(lse, H, T, q.device)
-    _check_ints(q.device, cu_seqlens=cu_seqlens)
-    with _on(q.device):
-        return load().fa2_fwd_varlen(_packed(q), _packed(k), _packed(v), _packed(o), lse.data_ptr(),
-                                     cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T, H, Hkv, d,
-                                     scale, int(bool(causal)), int(window), _dtype_code(q),
-                                     _stream(stream))
+    dev, dt, code = _device_of(q), q.dtype, _dtype_code(q)
+    T, H, d = shape = _dims("q", q, 3)
+    Hkv = _dims("k", k, 3)[1]
+    n = cu_seqlens.numel()
+    return _call(load().fa2_fwd_varlen, dev, stream, _rows("q", q, shape, dt, dev),
+                 _rows("k", k, (T, Hkv, d), dt, dev), _rows("v", v, (T, Hkv, d), dt, dev),
+                 _rows("o", o, shape, dt, dev), _lse(lse, H, T, dev),
+                 _ints("cu_seqlens", cu_seqlens, n, dev), n - 1, T, H, Hkv, d, scale,
+                 1 if causal else 0, window, code)
 
 
 def fa2_bwd_varlen_workspace_size(B: int, T: int, H: int, Hkv: int, d: int) -> int:
-    return int(load().fa2_bwd_varlen_workspace_size(B, T, H, Hkv, d))
+    return load().fa2_bwd_varlen_workspace_size(B, T, H, Hkv, d)
 
 
 def fa2_bwd_varlen(q, k, v, o, do, lse, dq, dk, dv, cu_seqlens, workspace, scale: float,
                    causal: bool, window: int = 0, stream=None) -> int:
     """Raw call of the packed backward; ``workspace`` is a uint8 CUDA tensor."""
-    _check_rows(q.dtype, q, k, v, o, do, dq, dk, dv)
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    _same_shape((T, Hkv, d), k=k, v=v, dk=dk, dv=dv)
-    _same_shape(q.shape, o=o, do=do, dq=dq)
-    _check_lse(lse, H, T, q.device)
-    _check_ints(q.device, cu_seqlens=cu_seqlens)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(q.device):
-        return load().fa2_bwd_varlen(_packed(q), _packed(k), _packed(v), _packed(o), _packed(do),
-                                     lse.data_ptr(), _packed(dq), _packed(dk), _packed(dv),
-                                     cu_seqlens.data_ptr(), _ptr(workspace), ws_bytes,
-                                     cu_seqlens.numel() - 1, T, H, Hkv, d, scale,
-                                     int(bool(causal)), int(window), _dtype_code(q),
-                                     _stream(stream))
-
-
-def _check_caches(*cs) -> None:
-    for c in cs:
-        if c.dim() != 4 or not c.is_cuda or (c.stride(3) != 1 and c.shape[3] != 1):
-            raise ValueError("caches must be [blocks, heads, block_size, d] CUDA tensors with "
-                             "contiguous columns")
+    dev, dt, code = _device_of(q), q.dtype, _dtype_code(q)
+    T, H, d = shape = _dims("q", q, 3)
+    Hkv = _dims("k", k, 3)[1]
+    kv = (T, Hkv, d)
+    n = cu_seqlens.numel()
+    return _call(load().fa2_bwd_varlen, dev, stream, _rows("q", q, shape, dt, dev),
+                 _rows("k", k, kv, dt, dev), _rows("v", v, kv, dt, dev),
+                 _rows("o", o, shape, dt, dev), _rows("do", do, shape, dt, dev),
+                 _lse(lse, H, T, dev), _rows("dq", dq, shape, dt, dev),
+                 _rows("dk", dk, kv, dt, dev), _rows("dv", dv, kv, dt, dev),
+                 _ints("cu_seqlens", cu_seqlens, n, dev), *_bytes(workspace, dev), n - 1, T, H,
+                 Hkv, d, scale, 1 if causal else 0, window, code)
 
 
 def fa2_fwd_paged_workspace_size(B: int, T: int, H: int, Hkv: int, d: int,
                                  sm_count: int = 0) -> int:
-    return int(load().fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, sm_count))
+    return load().fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, sm_count)
 
 
 def fa2_fwd_paged(q, k_cache, v_cache, o, lse, block_table, cu_seqlens, seq_lens, workspace,
                   scale: float, causal: bool, window: int = 0, stream=None) -> int:
     """Raw call: q, o [T,H,d]; caches [blocks,Hkv,block_size,d]; lse [H,T] float32;
     block_table [B,max_blocks], cu_seqlens [B+1], seq_lens [B] int32."""
-    _check_rows(q.dtype, q, o)
-    _check_caches(k_cache, v_cache)
-    T, H, d = q.shape
-    blocks, Hkv, bs, _ = k_cache.shape
-    _same_shape((blocks, Hkv, bs, d), k_cache=k_cache, v_cache=v_cache)
-    _same_shape(q.shape, o=o)
-    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or k_cache.device != q.device or \
-            v_cache.device != q.device:
-        raise ValueError("caches must have the queries' dtype and device")
-    B, max_blocks = block_table.shape
-    _same_shape((B,), seq_lens=seq_lens)
-    _same_shape((B + 1,), cu_seqlens=cu_seqlens)
-    _check_lse(lse, H, T, q.device)
-    _check_ints(q.device, block_table=block_table, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(q.device):
-        return load().fa2_fwd_paged(_packed(q), _cache(k_cache), _cache(v_cache), _packed(o),
-                                    lse.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
-                                    block_table.data_ptr(), _ptr(workspace), ws_bytes, B, T, H,
-                                    Hkv, d, blocks, bs, max_blocks, scale, int(bool(causal)),
-                                    int(window), _dtype_code(q), _stream(stream))
+    dev, dt, code = _device_of(q), q.dtype, _dtype_code(q)
+    T, H, d = shape = _dims("q", q, 3)
+    blocks, Hkv, bs, dc = _dims("k_cache", k_cache, 4)
+    pages = (blocks, Hkv, bs, d)
+    B, most = _dims("block_table", block_table, 2)
+    return _call(load().fa2_fwd_paged, dev, stream, _rows("q", q, shape, dt, dev),
+                 _pages("k_cache", k_cache, pages, dt, dev),
+                 _pages("v_cache", v_cache, pages, dt, dev), _rows("o", o, shape, dt, dev),
+                 _lse(lse, H, T, dev), _ints("cu_seqlens", cu_seqlens, B + 1, dev),
+                 _ints("seq_lens", seq_lens, B, dev),
+                 _ints("block_table", block_table, B * most, dev), *_bytes(workspace, dev), B, T,
+                 H, Hkv, d, blocks, bs, most, scale, 1 if causal else 0, window, code)
 
 
 def fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu_seqlens, seq_lens,
@@ -415,43 +412,29 @@ def fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu_seqlen
     """Raw call: int32 tensors, context_lens and new_lens [B], free_blocks [num_free],
     block_table [B,max_blocks] (updated), cu_seqlens [B+1], seq_lens [B], positions and
     slots [T], used [1]."""
-    _check_ints(context_lens.device, context_lens=context_lens, new_lens=new_lens,
-                free_blocks=free_blocks, block_table=block_table, cu_seqlens=cu_seqlens,
-                seq_lens=seq_lens, positions=positions, slots=slots, used=used)
-    if not context_lens.is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    B, max_blocks = block_table.shape
-    T = slots.numel()
-    _same_shape((B,), context_lens=context_lens, new_lens=new_lens, seq_lens=seq_lens)
-    _same_shape((B + 1,), cu_seqlens=cu_seqlens)
-    _same_shape((T,), positions=positions, slots=slots)
-    _same_shape((1,), used=used)
-    with _on(context_lens.device):
-        return load().fa2_paged_tables(context_lens.data_ptr(), new_lens.data_ptr(),
-                                       free_blocks.data_ptr(), free_blocks.numel(),
-                                       block_table.data_ptr(), cu_seqlens.data_ptr(),
-                                       seq_lens.data_ptr(), positions.data_ptr(),
-                                       slots.data_ptr(), used.data_ptr(), B, T, int(block_size),
-                                       max_blocks, _stream(stream))
+    dev = _device_of(block_table)
+    B, most = _dims("block_table", block_table, 2)
+    free, T = free_blocks.numel(), slots.numel()
+    return _call(load().fa2_paged_tables, dev, stream,
+                 _ints("context_lens", context_lens, B, dev), _ints("new_lens", new_lens, B, dev),
+                 _ints("free_blocks", free_blocks, free, dev), free,
+                 _ints("block_table", block_table, B * most, dev),
+                 _ints("cu_seqlens", cu_seqlens, B + 1, dev), _ints("seq_lens", seq_lens, B, dev),
+                 _ints("positions", positions, T, dev), _ints("slots", slots, T, dev),
+                 _ints("used", used, 1, dev), B, T, block_size, most)
 
 
 def fa2_paged_append(k, v, k_cache, v_cache, slots, stream=None) -> int:
     """Raw call: k, v [T,Hkv,d], caches [blocks,Hkv,block_size,d], slots [T] int32."""
-    _check_rows(k.dtype, k, v)
-    _check_caches(k_cache, v_cache)
+    dev, dt = _device_of(k), k.dtype
     _dtype_code(k)
-    T, Hkv, d = k.shape
-    blocks, _, bs, _ = k_cache.shape
-    _same_shape(k.shape, v=v)
-    _same_shape((blocks, Hkv, bs, d), k_cache=k_cache, v_cache=v_cache)
-    _same_shape((T,), slots=slots)
-    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype or k_cache.device != k.device or \
-            v_cache.device != k.device:
-        raise ValueError("caches must have the dtype and device of k and v")
-    _check_ints(k.device, slots=slots)
-    with _on(k.device):
-        return load().fa2_paged_append(_packed(k), _packed(v), _cache(k_cache), _cache(v_cache),
-                                       slots.data_ptr(), T, Hkv, d, blocks, bs, _stream(stream))
+    T, Hkv, d = shape = _dims("k", k, 3)
+    blocks, _, bs, _ = _dims("k_cache", k_cache, 4)
+    pages = (blocks, Hkv, bs, d)
+    return _call(load().fa2_paged_append, dev, stream, _rows("k", k, shape, dt, dev),
+                 _rows("v", v, shape, dt, dev), _pages("k_cache", k_cache, pages, dt, dev),
+                 _pages("v_cache", v_cache, pages, dt, dev), _ints("slots", slots, T, dev), T, Hkv,
+                 d, blocks, bs)
 
 
 def fa2_get_device_status(stream=None) -> tuple[int, int]:
@@ -576,9 +559,9 @@ def forward_varlen(q, k, v, cu_seqlens, scale: float, causal: bool, window: int 
     """Attention over packed sequences: O [T,H,d] and LSE [H,T] of q [T,H,d] and k, v
     [T,Hkv,d], sequence b being rows cu_seqlens[b] .. cu_seqlens[b+1] - 1.  Rows behind
     the last sequence are not written (fa2_fwd_varlen takes outputs of your own)."""
-    T, H, d = q.shape
-    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    T, H, d = _dims("q", q, 3)
+    o = q.new_empty((T, H, d))
+    lse = q.new_empty((H, T), dtype=torch.float32)
     rc = fa2_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, window, stream)
     if rc != FA2_OK:
         raise FA2Error(rc, "fa2_fwd_varlen")
@@ -589,14 +572,13 @@ def backward_varlen(q, k, v, o, do, lse, cu_seqlens, scale: float, causal: bool,
                     workspace=None, stream=None):
     """Gradients dQ [T,H,d], dK and dV [T,Hkv,d] of forward_varlen; the workspace is
     allocated if not given."""
-    T, H, d = q.shape
-    Hkv = k.shape[1]
+    T, H, d = _dims("q", q, 3)
+    Hkv = _dims("k", k, 3)[1]
     if workspace is None:
         n = fa2_bwd_varlen_workspace_size(cu_seqlens.numel() - 1, T, H, Hkv, d)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    dq = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    dk = torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device)
-    dv = torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device)
+        workspace = q.new_empty(n, dtype=torch.uint8)
+    dq = q.new_empty((T, H, d))
+    dk, dv = q.new_empty((T, Hkv, d)), q.new_empty((T, Hkv, d))
     rc = fa2_bwd_varlen(q, k, v, o, do, lse, dq, dk, dv, cu_seqlens, workspace, scale, causal,
                         window, stream)
     if rc != FA2_OK:
@@ -604,18 +586,23 @@ def backward_varlen(q, k, v, o, do, lse, cu_seqlens, scale: float, causal: bool,
     return dq, dk, dv
 
 
+@functools.lru_cache(maxsize=None)
+def _sm_count(dev: int) -> int:
+    return torch.cuda.get_device_properties(dev).multi_processor_count
+
+
 def forward_paged(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scale: float,
                   causal: bool, window: int = 0, workspace=None, stream=None):
     """Attention of a step's new tokens q [T,H,d] over paged caches
     [blocks,Hkv,block_size,d]: O [T,H,d] and LSE [H,T].  The workspace is allocated if
     not given."""
-    T, H, d = q.shape
+    T, H, d = _dims("q", q, 3)
     if workspace is None:
-        with _on(q.device):
-            n = fa2_fwd_paged_workspace_size(block_table.shape[0], T, H, k_cache.shape[1], d)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        n = fa2_fwd_paged_workspace_size(block_table.shape[0], T, H, k_cache.shape[1], d,
+                                         _sm_count(_device_of(q)))
+        workspace = q.new_empty(n, dtype=torch.uint8)
+    o = q.new_empty((T, H, d))
+    lse = q.new_empty((H, T), dtype=torch.float32)
     rc = fa2_fwd_paged(q, k_cache, v_cache, o, lse, block_table, cu_seqlens, seq_lens, workspace,
                        scale, causal, window, stream)
     if rc != FA2_OK:
@@ -628,10 +615,8 @@ def paged_tables(context_lens, new_lens, free_blocks, block_table, T: int, block
     """Tables of a step of at most T new tokens: (block_table, updated in place,
     cu_seqlens [B+1], seq_lens [B], positions [T], slots [T], used [1])."""
     B = block_table.shape[0]
-    ints = dict(dtype=torch.int32, device=block_table.device)
-    cu, lens = torch.empty(B + 1, **ints), torch.empty(B, **ints)
-    positions, slots = torch.empty(T, **ints), torch.empty(T, **ints)
-    used = torch.empty(1, **ints)
+    empty = block_table.new_empty
+    cu, lens, positions, slots, used = empty(B + 1), empty(B), empty(T), empty(T), empty(1)
     rc = fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu, lens, positions,
                           slots, used, block_size, stream)
     if rc != FA2_OK:

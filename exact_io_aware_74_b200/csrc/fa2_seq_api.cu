@@ -102,16 +102,25 @@ fa2::SeqParams seq_params(const fa2_packed* O, float* LSE, const int* cu, unsign
   return p;
 }
 
-// Query tiles of a paged item: two where the requests bring more than a tile of rows on
-// average (prompts, chunks), one for decode steps, whose second tile would be empty.
-int paged_tiles(int B, int T, int G, int d) { return d <= 128 && T > static_cast<long long>(128 / G) * B ? 2 : 1; }
+// Form of a paged call's items, by the rows that the requests bring on average: two query
+// tiles of 128 rows (prompts, chunks), one, or 32 or 16 rows with the products' operands
+// swapped (decode steps; d <= 128).  Every form is right for every batch.
+int paged_form(int B, int T, int G, int d) {
+  if (d > 128) return 1;
+  const long long rows = static_cast<long long>(T) * G, b = B;
+  if (G <= 16 && rows <= 16 * b) return 16;
+  if (G <= 32 && rows <= 32 * b) return 32;
+  return T > 128 / G * b ? 2 : 1;
+}
+int form_tiles(int form) { return form == 2 ? 2 : 1; }           // 128-row tiles of a partial slot
+int form_tokens(int form, int G) { return (form > 2 ? form : 128) / G; }  // tokens to a tile
 
-// Float partials of the shares: two slots each, O then LSE.
+// Float partials of the shares, two slots each: O, then LSE, then what is to be merged.
 size_t paged_opart_bytes(int grid, int qt, int d) {
   return static_cast<size_t>(grid) * 2 * qt * 128 * fa2::seq_tile_dim(d) * 4;
 }
 size_t paged_bytes(int grid, int qt, int d) {
-  return paged_opart_bytes(grid, qt, d) + static_cast<size_t>(grid) * 2 * qt * 128 * 4;
+  return paged_opart_bytes(grid, qt, d) + static_cast<size_t>(grid) * (2 * qt * 128 * 4 + sizeof(int4));
 }
 
 // ---- backward ----
@@ -289,7 +298,7 @@ size_t fa2_fwd_paged_workspace_size(int B, int T, int H, int Hkv, int d, int sm_
       return 0;
     }
   }
-  return (paged_bytes(sm_count, paged_tiles(B, T, H / Hkv, d), d) + 255) / 256 * 256;
+  return (paged_bytes(sm_count, form_tiles(paged_form(B, T, H / Hkv, d)), d) + 255) / 256 * 256;
 }
 
 int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, const fa2_packed* O,
@@ -323,20 +332,22 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, n_sm))
     return FA2_ERR_WORKSPACE;
-  const int G = H / Hkv, qt = paged_tiles(B, T, G, d);
+  const int G = H / Hkv, form = paged_form(B, T, G, d), tpt = form_tokens(form, G);
   fa2::SeqMaps m;
-  if (!map_packed(&m.q, Q, T, H, d, dtype, false, 128 / G, G) ||
+  if (!map_packed(&m.q, Q, T, H, d, dtype, false, tpt, G) ||
       !map_cache(&m.k, K, num_blocks, Hkv, block_size, d, dtype) ||
       !map_cache(&m.v, V, num_blocks, Hkv, block_size, d, dtype))
     return FA2_ERR_CUDA;
   fa2::SeqParams p = seq_params(O, LSE, cu_seqlens, st, B, T, H, Hkv, d, scale, causal, window);
+  p.tpt = tpt;
   p.seq_lens = seq_lens;
   p.block_table = block_table;
   p.num_blocks = num_blocks, p.block_size = block_size, p.max_blocks = max_blocks;
   p.box_rows = std::min(block_size, 128);
   p.O_part = static_cast<float*>(workspace);
-  p.LSE_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_opart_bytes(n_sm, qt, d));
-  return fa2::launch_seq_paged(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(n_sm),
+  p.LSE_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_opart_bytes(n_sm, form_tiles(form), d));
+  p.merge = reinterpret_cast<int4*>(p.LSE_part + static_cast<size_t>(n_sm) * 2 * form_tiles(form) * 128);
+  return fa2::launch_seq_paged(d, dtype == FA2_BF16, form, m, p, dev, static_cast<unsigned int>(n_sm),
                                reinterpret_cast<cudaStream_t>(stream));
 }
 

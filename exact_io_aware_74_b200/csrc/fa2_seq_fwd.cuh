@@ -47,6 +47,7 @@ struct SeqParams {
   const int* block_table;   // paged: [B][max_blocks]
   float* O_part;            // [2 grid][QT * 128][D]
   float* LSE_part;          // [2 grid][QT * 128]
+  int4* merge;              // [grid]: the cut block that starts in the share (row, tokens, head, parts)
   unsigned int* status;
   unsigned long long wait_ns;
   int B, T, Hkv, G, d, tpt;  // tpt: tokens to a tile, 128 / G
@@ -56,25 +57,33 @@ struct SeqParams {
   float scale_log2;
 };
 
-template <int D_, int QT_>
+// NQ = 0: the layout above.  NQ = 16 or 32 (QT = 1): items of at most NQ rows, with the
+// operands of both products swapped (see the few-rows roles of the kernel).
+template <int D_, int QT_, int NQ_ = 0>
 struct SeqCfg {
-  static constexpr int D = D_, QT = QT_;
+  static constexpr int D = D_, QT = QT_, NQ = NQ_;
   static_assert(QT == 1 || D <= 128, "two accumulators fit tensor memory up to D = 128");
+  static_assert(NQ == 0 || (QT == 1 && D <= 128 && (NQ == 16 || NQ == 32)), "few rows");
   static constexpr int KCH = D / 64;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = 128 * D * 2;
+  static constexpr int QCHUNK = NQ ? NQ * 128 : CHUNK, QTILE = KCH * QCHUNK;
   // Ring stages within 227 KB (tiles of 16, 32, 48, 64 KB).  Two query tiles have a third
   // slot at D = 128, so that the next item's first tile loads during this one.
-  static constexpr int QS = D == 64 ? 4 : (D == 128 ? (QT == 2 ? 3 : 2) : 1);
-  static constexpr int KS = D == 64 ? 4 : (D == 256 ? 1 : 2);
-  static constexpr int VS = D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1);
-  static constexpr int SMEM = (QS + KS + VS) * TILE + 1024;
+  static constexpr int QS = NQ ? 2 : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 3 : 2) : 1));
+  static constexpr int KS = NQ ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : (D == 256 ? 1 : 2));
+  static constexpr int VS = NQ ? KS : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1));
+  // Few rows: P^T of each warpgroup, two chunks of 64 keys.  (At D = 64 the V operand's
+  // upper 64 rows are whatever lies 16 KB behind the tile: at least that much follows.)
+  static constexpr int PBUF = 2 * NQ * 128;
+  static constexpr int REST = NQ ? (QS * QTILE + 2 * PBUF < CHUNK ? CHUNK : QS * QTILE + 2 * PBUF) : QS * TILE;
+  static constexpr int SMEM = (KS + VS) * TILE + REST + 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory");
   static constexpr int THREADS = 384;
   static constexpr int LAUNCH_REGS = 168;
   static constexpr int SOFT_REGS = 216, OTHER_REGS = 72;
   static_assert(2 * 128 * SOFT_REGS + 128 * OTHER_REGS <= THREADS * LAUNCH_REGS, "register re-split");
-  __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256u + t * D; }
+  __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256u + t * (NQ ? NQ : D); }
   // D = 64 with two tiles: P in columns of its own (the next scores overwrite S early).
   static constexpr bool SEP = D == 64 && QT == 2;
   __host__ __device__ static constexpr uint32_t P_COL(int t) { return 384u + 64u * t; }
@@ -164,32 +173,32 @@ __device__ __forceinline__ void cut_item(SeqItem& it, int a, int e) {
   it.n = max(it.hi[0], it.hi[1]) - it.j0;
 }
 
-// Units of work of block blk of a sequence: its key tiles, at least one.
+// Units of work of block blk of a sequence: its key tiles (both query tiles' together),
+// at least one.
 template <int QT>
-__device__ __forceinline__ int block_units(const SeqParams& p, const SeqLen& s, int blk) {
-  const int R = QT * p.tpt, a = blk * R, e = min(s.n, a + R), m = min(e, a + p.tpt);
-  int l0, h0, l1 = 0, h1 = 0;
-  key_range(p, s, a, m, l0, h0);
-  if (QT == 2) key_range(p, s, m, e, l1, h1);
-  const int lo = h0 > 0 ? (h1 > 0 ? min(l0, l1) : l0) : l1;
-  return max(1, max(h0, h1) - lo);
+__device__ __forceinline__ int block_units(const SeqParams& p, int n, int nk, int blk) {
+  const int a = blk * (QT * p.tpt);
+  int lo, hi;
+  key_range(p, SeqLen{0, n, nk}, a, min(n, a + QT * p.tpt), lo, hi);
+  return max(1, hi - lo);
 }
+__device__ __forceinline__ int blocks_of(int n, int R) { return n <= R ? (n > 0) : (n + R - 1) / R; }
 
-// Units of one key/value head of a sequence per lane: lanes with few blocks sum their own,
-// the others' are summed by the whole warp.
+// Units of one key/value head of a sequence per lane: of a single block each lane its own,
+// of more the whole warp together.
 template <int QT>
 __device__ __forceinline__ int lane_units(const SeqParams& p, int n, int nk, int lane) {
-  const int R = QT * p.tpt, nb = (n + R - 1) / R;
-  int u = 0;
-  if (nb <= 4)
-    for (int i = 0; i < nb; ++i) u += block_units<QT>(p, SeqLen{0, n, nk}, i);
-  unsigned int many = __ballot_sync(0xffffffffu, nb > 4);
+  const int R = QT * p.tpt;
+  int u = n > 0 ? block_units<QT>(p, n, nk, 0) : 0;
+  unsigned int many = __ballot_sync(0xffffffffu, n > R);
+#pragma unroll 1
   while (many) {
     const int l = __ffs(many) - 1;
     many &= many - 1;
-    const SeqLen o{0, __shfl_sync(0xffffffffu, n, l), __shfl_sync(0xffffffffu, nk, l)};
+    const int on = __shfl_sync(0xffffffffu, n, l), ok = __shfl_sync(0xffffffffu, nk, l);
     int part = 0;
-    for (int i = lane; i < (o.n + R - 1) / R; i += 32) part += block_units<QT>(p, o, i);
+#pragma unroll 1
+    for (int i = lane; i * R < on; i += 32) part += block_units<QT>(p, on, ok, i);
     part = __reduce_add_sync(0xffffffffu, part);
     if (lane == l) u = part;
   }
@@ -205,13 +214,14 @@ __device__ __forceinline__ int warp_inclusive(int x, int lane) {
   return x;
 }
 
-// CTAs that get a share: at least kMinUnits units each.
+// Units to a share: equal for `grid` CTAs (the last ones may get fewer or none), at least
+// kMinUnits.  32-bit division wherever it will do: this is the first code that every CTA
+// runs, from a cold instruction cache.
 constexpr int kMinUnits = 2;
-__device__ __forceinline__ int share_ctas(long long units, int grid) {
-  const long long c = (units + kMinUnits - 1) / kMinUnits;
-  return static_cast<int>(c < grid ? (c > 0 ? c : 1) : grid);
+__device__ __forceinline__ long long share_units(long long total, int grid) {
+  if (total < (1ll << 31)) return max((static_cast<unsigned int>(total) + grid - 1) / static_cast<unsigned int>(grid), kMinUnits + 0u);
+  return static_cast<long long>(static_cast<unsigned int>(total >> 16) / static_cast<unsigned int>(grid) + 1) << 16;
 }
-__device__ __forceinline__ long long share_start(long long units, int ctas, int c) { return units * c / ctas; }
 
 // The linear order of the units: sequence, head, block, key tile.  Whole warp.
 struct UnitAt {
@@ -219,29 +229,25 @@ struct UnitAt {
   SeqLen s;
 };
 
-// Cuts the units of all items into shares, at most `grid` of them, and finds where share
-// `c` starts: false when there is no such share.  x, xe: its units; `held`: kHeld ints of
-// shared memory (or nullptr: the units are computed twice).  One loop body serves the
-// total and the search: this code runs once a CTA, and the instruction cache is better
-// left to the loops that run on.
+// Finds share c: units x .. xe - 1, `per` to a share.  False when there is none.  held:
+// kHeld ints of shared memory.  One loop body serves the total and the search.
 template <int QT>
-__device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, int* held, int lane, int& ctas,
-                                           long long& total, long long& x, long long& xe, UnitAt& r) {
-  total = 0;
+__device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, int* held, int lane, long long& per,
+                                           long long& x, long long& xe, UnitAt& r) {
+  long long total = 0, rem = 0;
   int units = 1;  // of one head of the sequence found
-  long long rem = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       int v;
-      if (pass == 1 && held && b0 < kHeld) {
+      if (pass == 1 && b0 < kHeld) {
         v = held[b0 + lane];
       } else {
         SeqLen s{0, 0, 0};
         if (b0 + lane < p.B) s = seq_len<true>(p, b0 + lane);
         v = lane_units<QT>(p, s.n, s.nk, lane);
-        if (pass == 0 && held && b0 < kHeld) held[b0 + lane] = v;
+        if (b0 < kHeld) held[b0 + lane] = v;
       }
       const int inc = warp_inclusive(v, lane);
       const long long end = static_cast<long long>(inc) * p.Hkv;
@@ -260,30 +266,34 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
       rem -= __shfl_sync(0xffffffffu, end, 31);
     }
     if (pass == 0) {
-      ctas = share_ctas(total, grid);
-      if (c >= ctas || total == 0) return false;
-      x = rem = share_start(total, ctas, c);
-      xe = share_start(total, ctas, c + 1);
+      per = share_units(total, grid);
+      x = rem = per * c;
+      xe = min(total, x + per);
+      if (x >= total) return false;
       __syncwarp();
     }
   }
   r.s = seq_len<true>(p, r.b);
-  r.kvh = static_cast<int>(rem / units);
+  // A sequence's units are below 2^31 for one head, its heads' together perhaps not.
+  r.kvh = rem < (1ll << 31) ? static_cast<unsigned int>(rem) / static_cast<unsigned int>(units)
+                            : static_cast<int>(rem / units);
   int at = static_cast<int>(rem - static_cast<long long>(r.kvh) * units);
-  const int R = QT * p.tpt, nb = (r.s.n + R - 1) / R;
+  const int R = QT * p.tpt, nb = blocks_of(r.s.n, R);
   r.blk = 0;
+  if (nb > 1) {
 #pragma unroll 1
-  for (int i0 = 0; i0 < nb; i0 += 32) {
-    const int v = i0 + lane < nb ? block_units<QT>(p, r.s, i0 + lane) : 0;
-    const int inc = warp_inclusive(v, lane);
-    const unsigned int m = __ballot_sync(0xffffffffu, inc > at);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      r.blk = i0 + l;
-      at -= __shfl_sync(0xffffffffu, inc - v, l);
-      break;
+    for (int i0 = 0; i0 < nb; i0 += 32) {
+      const int v = i0 + lane < nb ? block_units<QT>(p, r.s.n, r.s.nk, i0 + lane) : 0;
+      const int inc = warp_inclusive(v, lane);
+      const unsigned int m = __ballot_sync(0xffffffffu, inc > at);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        r.blk = i0 + l;
+        at -= __shfl_sync(0xffffffffu, inc - v, l);
+        break;
+      }
+      at -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    at -= __shfl_sync(0xffffffffu, inc, 31);
   }
   r.at = at;
   return true;
@@ -459,17 +469,18 @@ __device__ __forceinline__ void tile_keys(const SeqItem& it, int j, int& a, int&
   e = min(it.nk - j * 128, 128);
 }
 
-template <int D, bool BF16, int QT, bool PAGED>
+template <int D, bool BF16, int QT, bool PAGED, int NQ>
 __global__ void __launch_bounds__(384, 1)
 fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const SeqParams p) {
-  using C = SeqCfg<D, QT>;
+  using C = SeqCfg<D, QT, NQ>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sK = sQ + C::QS * C::TILE;
+  uint8_t* sK = smem;
   uint8_t* sV = sK + C::KS * C::TILE;
+  uint8_t* sQ = sV + C::VS * C::TILE;
+  [[maybe_unused]] uint8_t* sP = sQ + C::QS * C::QTILE;  // few rows: P^T, one buffer to a warpgroup
 
   __shared__ __align__(16) uint4 clc_response;
   constexpr int NI = kSeqItems;
@@ -477,7 +488,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __shared__ uint64_t item_full[NI], item_empty[NI], clc_full;
   __shared__ uint64_t q_full[C::QS], q_empty[C::QS], k_full[C::KS], k_empty[C::KS];
   __shared__ uint64_t v_full[C::VS], v_empty[C::VS], v_raw[C::VS];
-  __shared__ uint64_t s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2], drain;
+  __shared__ uint64_t s_full[4], s_free[4], p_ready[2], o_done[2], o_free[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int held[kHeld];  // the scheduling warp's
@@ -492,14 +503,16 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     abort_flag = 0;
     for (int i = 0; i < NI; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 3 + 4 * QT);  // producer, MMA, V fix and the softmax warps
+      mbar_init(&item_empty[i], 3 + (NQ ? 8 : 4 * QT));  // producer, MMA, V fix and the softmax warps
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&p_ready[i], 4);
       mbar_init(&o_done[i], 1);
-      mbar_init(&o_free[i], 4);
+      mbar_init(&o_free[i], NQ ? 8 : 4);
     }
     mbar_init(&clc_full, 1);
     for (int i = 0; i < C::QS; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
@@ -545,17 +558,23 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       bool ok = true;
       if constexpr (PAGED) {
         const int c = blockIdx.x;
-        int ctas;
-        long long units, x, xe;
+        if (lane == 0) p.merge[c] = make_int4(0, 0, 0, 0);  // nothing to merge, until a block is cut
+        long long per, x, xe;
         UnitAt u;
-        if (find_share<QT>(p, gridDim.x, c, held, lane, ctas, units, x, xe, u) && x < xe) {
+        if (find_share<QT>(p, gridDim.x, c, held, lane, per, x, xe, u)) {
           const int R = QT * p.tpt;
 #pragma unroll 1
           while (ok) {
-            const int len = block_units<QT>(p, u.s, u.blk);
+            const int len = block_units<QT>(p, u.s.n, u.s.nk, u.blk);
             const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
             make_item<true, QT>(p, u.s, u.b, u.kvh, u.blk, it);
             if (u.at > 0 || take < len) {
+              if (u.at == 0 && lane == 0) {
+                // The block starts here and goes on in the next shares: for the merge kernel.
+                int parts = 1;
+                for (long long e = xe; e < x + len; e += per) ++parts;
+                p.merge[c] = make_int4(it.row0, it.n_tok, u.kvh, parts);
+              }
               cut_item(it, u.at, u.at + take);
               it.part = 2 * c + (u.at > 0 ? 0 : 1);
             }
@@ -563,7 +582,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             x += take;
             if (x >= xe) break;
             u.at = 0;
-            if (++u.blk >= (u.s.n + R - 1) / R) {
+            if (++u.blk * R >= u.s.n) {
               u.blk = 0;
               if (++u.kvh >= p.Hkv) {
                 u.kvh = 0;
@@ -621,7 +640,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (lane == 0) {
           mbar_arrive_expect_tx(&q_full[s], C::KCH * 128 * p.G * p.tpt);
           for (int c = 0; c < C::KCH; ++c)
-            tma_load_3d(sQ + s * C::TILE + c * C::CHUNK, &tmQ, &q_full[s], c * 64, it.kvh * p.G,
+            tma_load_3d(sQ + s * C::QTILE + c * C::QCHUNK, &tmQ, &q_full[s], c * 64, it.kvh * p.G,
                         it.row0 + t * p.tpt);
         }
         ++qc;
@@ -697,8 +716,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const int j = it.j0 + jj;
           const int pg_next = PAGED && jj + 1 < it.n ? pages_of(it, j + 1) : 0;
           ok = load_k(it, j, pg);
-          if (QT == 2) {
-            if (ok && jj == 0 && it.hi[1] > 0) ok = load_q(it, 1);
+          if (QT == 2 || NQ) {
+            if (QT == 2 && ok && jj == 0 && it.hi[1] > 0) ok = load_q(it, 1);
             ok = ok && load_v(it, j, pg);
           } else {
             if (ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
@@ -709,7 +728,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           pg = pg_next;
         }
       }
-      if (QT == 1 && ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
+      if (QT == 1 && !NQ && ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
       if (lane == 0) {
         // Every copy that was issued lands before the CTA leaves, on a timeout too.
         volatile int no_abort = 0;
@@ -755,7 +774,89 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
       }
       __syncwarp();
-    } else if (lane == 0) {
+    } else if (NQ > 0 && lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer, few rows
+      // S^T = K Q^T (128 keys x NQ rows) runs kLag steps ahead of O^T += V^T P^T (head columns
+      // x NQ rows); step c is warpgroup c & 1's, with an accumulator of its own.
+      constexpr int N = NQ ? NQ : 16;  // (NQ = 0: not reached)
+      constexpr int kLag = 2;
+      constexpr uint32_t id_s = idesc_f16(128, N, BF16, false, false);
+      constexpr uint32_t id_o = idesc_f16(128, N, BF16, true, false);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_u32(sV), C::CHUNK, 1024), dP = sdesc_sw128(smem_u32(sP), 16, 1024);
+      int ii = 0, qc = 0;
+      int c = 0;                 // steps whose S has been issued
+      int left = 0;              // steps of the current item still to issue
+      int begun = 0;             // steps of the current item issued
+      int oc0 = 0, oc1 = 0;      // items begun per accumulator
+      unsigned int first = 0;    // bit 0: the newest step was the first of its accumulator in its item
+      bool ok = true, more = true;
+      for (int i = 0; ok; ++i) {
+        if (left == 0 && more) {
+          for (;; ++ii) {  // the next item with key tiles
+            ok = mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem);
+            if (!ok) break;
+            more = items[ii % NI].valid != 0;
+            left = more ? items[ii % NI].n : 0;
+            mbar_arrive(&item_empty[ii % NI]);
+            if (!more || left > 0) break;
+          }
+          if (!ok) break;
+          ++ii;
+          begun = 0;
+          if (more) ok = mbar_wait(&q_full[qc % C::QS], (qc / C::QS) & 1, wc, kQSiteMmaQ);
+          if (!ok) break;
+        }
+        first <<= 1;
+        if (left > 0) {
+          const int b = c & 3, ks = c % C::KS;
+          ok = mbar_wait(&k_full[ks], (c / C::KS) & 1, wc, kQSiteMmaK);
+          if (ok && c >= 4) ok = mbar_wait(&s_free[b], ((c >> 2) - 1) & 1, wc, kQSiteMmaP);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = sdesc_add(dK, ks * C::TILE), db = sdesc_add(dQ, (qc % C::QS) * C::QTILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tbase + b * N, sdesc_add(da, (kk >> 2) * C::CHUNK + (kk & 3) * 32),
+                    sdesc_add(db, (kk >> 2) * C::QCHUNK + (kk & 3) * 32), id_s, kk > 0);
+          umma_commit(&s_full[b]);
+          umma_commit(&k_empty[ks]);
+          if (--left == 0) {
+            umma_commit(&q_empty[qc % C::QS]);
+            ++qc;
+          }
+          first |= begun < 2 ? 1u : 0u;
+          ++begun;
+          ++c;
+        } else if (i >= c + kLag) {
+          break;  // nothing left to issue and every P V is out
+        }
+        const int e = i - kLag;  // step of this round's P V
+        if (e < 0 || e >= c) continue;
+        const int w = e & 1, vs = e % C::VS;
+        const bool new_item = first >> kLag & 1;
+        ok = mbar_wait(&v_full[vs], (e / C::VS) & 1, wc, kQSiteMmaV) &&
+             mbar_wait(&p_ready[w], (e >> 1) & 1, wc, kQSiteMmaP);
+        if (ok && new_item) {
+          int& oc = w ? oc1 : oc0;
+          if (oc > 0) ok = mbar_wait(&o_free[w], (oc - 1) & 1, wc, kQSiteMmaO);
+          ++oc;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t da = sdesc_add(dV, vs * C::TILE), db = sdesc_add(dP, w * C::PBUF);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ss(tbase + C::O_COL(w), sdesc_add(da, kk * 2048),
+                  sdesc_add(db, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_o, (kk > 0 || !new_item) ? 1u : 0u);
+        umma_commit(&o_done[w]);
+        umma_commit(&v_empty[vs]);
+      }
+      umma_commit(&drain);
+      volatile int no_abort = 0;
+      WaitCtl dw{p.status, &no_abort, p.wait_ns};
+      mbar_wait(&drain, 0, dw, kQSiteMmaDrain);
+    } else if (NQ == 0 && lane == 0) {
       // ---------------------------------------------------------------- MMA issuer (warp 9)
       // One loop over the key tiles of all items.  Step j issues P V of its own tile and S of
       // the step after it, which may be the next item's first; the loop begins with a step
@@ -811,7 +912,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           k_ok = true;
           tc_fence_after();
           const int b = QT == 2 ? t : (sc & 1);
-          const uint64_t da = sdesc_add(dQ, qs * C::TILE), db = sdesc_add(dK, ks * C::TILE);
+          const uint64_t da = sdesc_add(dQ, qs * C::QTILE), db = sdesc_add(dK, ks * C::TILE);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
@@ -897,6 +998,229 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       mbar_wait(&drain, 0, dw, kQSiteMmaDrain);
     }
     __syncwarp();
+  } else if constexpr (NQ > 0) {
+    // ------------------------------------------------------------------ softmax, few rows
+    // A decode step has G rows to an item.  With the rows along the 128 lanes of a score
+    // tile, one warp of four would do all exponentials, 128 to a thread.  Here the keys lie
+    // along the lanes: thread r holds the NQ scores of key r, and the two warpgroups take the
+    // key tiles in turn, each with its own running maximum and accumulator; they are joined
+    // at the item's end.  The maximum is shared by the warpgroup and stale as in the other
+    // form: an exchange only when some score is more than 2^8 above it.
+    regs_inc<C::SOFT_REGS>();
+    constexpr int N = NQ;
+    const int w = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;  // key of the tile; head column of the output
+    const uint32_t lb = static_cast<uint32_t>(wq * 32);
+    const uint32_t wg_bar = 1 + w;
+    const int G = p.G;
+    const float sl2 = p.scale_log2;
+    uint8_t* myP = sP + w * C::PBUF;
+    int c = 0, pc = 0;  // steps before this item; steps of this warpgroup
+    for (int ii = 0;; ++ii) {
+      // Waits end in a vote of all that share a named barrier, which has no time limit.
+      if (!named_bar_and(3, 256, mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem))) break;
+      const SeqItem& it = items[ii % NI];  // held until the item is done
+      if (!it.valid) break;
+      const int steps = it.n, rows = it.n_tok * G, pos = it.pos, nk = it.nk, j0 = it.j0;
+      const int row0 = it.row0, kvh = it.kvh, part = it.part;
+      // Keys up to sure_hi and from sure_lo on are seen by every row.
+      const int sure_hi = p.causal ? min(pos, nk - 1) : nk - 1;
+      const int sure_lo = p.window > 0 ? pos + it.n_tok - p.window : 0;
+      float m[N], l[N], lr[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) m[n] = -INFINITY, l[n] = 0.f, lr[n] = 0.f;
+      bool ok = true;
+      const int s0 = (c & 1) == w ? 0 : 1;
+      for (int s = s0; s < steps; s += 2) {
+        const int b = (c + s) & 3;
+        // This step's scores, and P's buffer free of the product before.
+        bool got = mbar_wait(&s_full[b], ((c + s) >> 2) & 1, wc, kQSiteSoftS);
+        if (got && pc > 0) got = mbar_wait(&o_done[w], (pc - 1) & 1, wc, kQSiteSoftO);
+        ok = named_bar_and(wg_bar, 128, got);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[N];
+        if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, b * N), sr);
+        else tmem_ld32(tmem_addr(tbase, lb, b * N), sr);
+        tmem_wait_ld();
+        reg_fence(sr);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
+        const int kc0 = (j0 + s) * 128, key = kc0 + r;
+        const bool masked = kc0 + 127 > sure_hi || kc0 < sure_lo;
+        float x[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] = n < rows ? __uint_as_float(sr[n]) * sl2 : -INFINITY;
+        if (masked) {
+          int tok = 0, g = 0;
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const int kl = p.causal ? min(pos + tok, nk - 1) : nk - 1;
+            if (key > kl || (p.window > 0 && key <= pos + tok - p.window)) x[n] = -INFINITY;
+            if (++g == G) g = 0, ++tok;
+          }
+        }
+        bool need = s == s0;
+        float wm[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          wm[n] = -INFINITY;
+          if (n < rows) wm[n] = warp_max(x[n]);
+          need |= wm[n] - m[n] > 8.0f;
+        }
+        if (!named_bar_and(wg_bar, 128, !need)) {
+          float* ex = reinterpret_cast<float*>(myP);  // [4][N]
+          if (lane < N) {
+            float mine = wm[0];
+#pragma unroll
+            for (int n = 1; n < N; ++n) mine = lane == n ? wm[n] : mine;
+            ex[wq * N + lane] = mine;
+          }
+          named_bar_sync(wg_bar, 128);
+          float f[N];
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const float t = fmaxf(fmaxf(ex[n], ex[N + n]), fmaxf(ex[2 * N + n], ex[3 * N + n]));
+            const float mn = fmaxf(m[n], t);
+            f[n] = mn - m[n] > 0.f ? ex2_approx(m[n] - mn) : 1.0f;
+            m[n] = mn;
+            l[n] *= f[n];
+            lr[n] *= f[n];
+          }
+          if (s != s0) {  // the accumulator (its last product has been waited for)
+            uint32_t o[N];
+            if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, C::O_COL(w)), o);
+            else tmem_ld32(tmem_addr(tbase, lb, C::O_COL(w)), o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int n = 0; n < N; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
+            if constexpr (N == 16) tmem_st16(tmem_addr(tbase, lb, C::O_COL(w)), o);
+            else tmem_st32(tmem_addr(tbase, lb, C::O_COL(w)), o);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          named_bar_sync(wg_bar, 128);  // every warp has read the maxima: P may go over them
+        }
+        // P^T, K-major rows of 64 keys with 128-byte swizzle: 16-byte unit u of row n at u ^ (n % 8).
+        uint8_t* dst = myP + (r >> 6) * (N * 128) + (r & 7) * 2;
+        const int u = (r & 63) >> 3;
+#pragma unroll
+        for (int n = 0; n < N; n += 2) {
+          const float e0 = ex2_approx(x[n] - (m[n] == -INFINITY ? 0.f : m[n]));
+          const float e1 = ex2_approx(x[n + 1] - (m[n + 1] == -INFINITY ? 0.f : m[n + 1]));
+          const uint32_t pk = pack2<BF16>(e0, e1);
+          float r0, r1;
+          unpack2<BF16>(pk, r0, r1);
+          l[n] += e0;
+          l[n + 1] += e1;
+          lr[n] += r0;
+          lr[n + 1] += r1;
+          *reinterpret_cast<uint16_t*>(dst + n * 128 + ((u ^ (n & 7)) << 4)) = static_cast<uint16_t>(pk);
+          *reinterpret_cast<uint16_t*>(dst + (n + 1) * 128 + ((u ^ ((n + 1) & 7)) << 4)) = static_cast<uint16_t>(pk >> 16);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[w]);
+        ++pc;
+      }
+      // The item's end: the sums over the keys, then both warpgroups' parts joined.
+      const bool mine = steps > s0;  // this warpgroup had steps
+      if (ok && mine) ok = mbar_wait(&o_done[w], (pc - 1) & 1, wc, kQSiteSoftO);
+      float* ex = reinterpret_cast<float*>(myP);  // [4][2][N] sums, [N] maxima
+      if (steps > 0) {
+        // Lane n < N ends up with the warp's sums of row n.
+        float sl = 0.f, sr2 = 0.f, mm = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          if (n < rows) {
+            float a = l[n], q = lr[n];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              a += __shfl_xor_sync(0xffffffffu, a, o);
+              q += __shfl_xor_sync(0xffffffffu, q, o);
+            }
+            if (lane == n) sl = a, sr2 = q, mm = m[n];
+          }
+        }
+        // (P's buffer is free once this warpgroup's last product is done, for all its warps.)
+        ok = named_bar_and(wg_bar, 128, ok);
+        if (ok && lane < N) {
+          ex[(wq * 2) * N + lane] = sl;
+          ex[(wq * 2 + 1) * N + lane] = sr2;
+          if (wq == 0) ex[8 * N + lane] = mm;
+        }
+        tc_fence_before();
+      }
+      if (!named_bar_and(3, 256, ok)) break;
+      tc_fence_after();
+      constexpr int H2 = N / 2;  // rows of this warpgroup's half
+      const float* e0 = reinterpret_cast<const float*>(sP);
+      const float* e1 = reinterpret_cast<const float*>(sP + C::PBUF);
+      const int n0 = w * H2;
+      if (n0 < rows) {
+        uint32_t o0[H2], o1[H2];
+        if (steps > 0) {
+          if constexpr (H2 == 8) {
+            tmem_ld8(tmem_addr(tbase, lb, C::O_COL(0) + n0), o0);
+            tmem_ld8(tmem_addr(tbase, lb, C::O_COL(1) + n0), o1);
+          } else {
+            tmem_ld16(tmem_addr(tbase, lb, C::O_COL(0) + n0), o0);
+            tmem_ld16(tmem_addr(tbase, lb, C::O_COL(1) + n0), o1);
+          }
+          tmem_wait_ld();
+          reg_fence(o0);
+          reg_fence(o1);
+        }
+        // Which warpgroups have a part: with one step only the one whose turn it was.
+        const bool has0 = steps > 1 || (steps == 1 && (c & 1) == 0), has1 = steps > 1 || (steps == 1 && (c & 1) == 1);
+        int tok = n0 / G, g = n0 - tok * G;
+#pragma unroll
+        for (int i = 0; i < H2; ++i) {
+          const int n = n0 + i;
+          if (n < rows) {
+            const float m0 = has0 ? e0[8 * N + n] : -INFINITY, m1 = has1 ? e1[8 * N + n] : -INFINITY;
+            const float M = fmaxf(m0, m1);
+            const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
+            float L = 0.f, R = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (a0 > 0.f) L += a0 * e0[q * 2 * N + n], R += a0 * e0[(q * 2 + 1) * N + n];
+              if (a1 > 0.f) L += a1 * e1[q * 2 * N + n], R += a1 * e1[(q * 2 + 1) * N + n];
+            }
+            const float inv = (L > 0.f && R > 0.f) ? 1.0f / R : 0.f;
+            const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+            float y = a0 > 0.f ? a0 * __uint_as_float(o0[i]) : 0.f;
+            if (a1 > 0.f) y += a1 * __uint_as_float(o1[i]);
+            y *= inv;
+            const int row = row0 + tok, head = kvh * G + g;
+            if (part < 0) {
+              if (r < p.d)
+                p.O[row * p.o_row + head * p.o_head + r] = static_cast<uint16_t>(pack2<BF16>(y, 0.f));
+              if (r == 0) p.LSE[static_cast<size_t>(head) * p.T + row] = lse;
+            } else {
+              const size_t prow = static_cast<size_t>(part) * 128 + n;
+              if (r < D) p.O_part[prow * D + r] = y;
+              if (r == 0) p.LSE_part[prow] = lse;
+            }
+          }
+          if (++g == G) g = 0, ++tok;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (steps > 0) {
+          // An accumulator without steps in this item is not waited for.
+          if (steps > 1 || (c & 1) == 0) mbar_arrive(&o_free[0]);
+          if (steps > 1 || (c & 1) == 1) mbar_arrive(&o_free[1]);
+        }
+        mbar_arrive(&item_empty[ii % NI]);
+      }
+      c += steps;
+    }
   } else {
     // ------------------------------------------------------------------ softmax
     regs_inc<C::SOFT_REGS>();
@@ -1119,51 +1443,62 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 // merge of the partials
 // ------------------------------------------------------------------------------------
 
-// CTA x looks at the boundary between shares x and x + 1.  If it is the first boundary
-// inside a block of rows, the shares that hold the block are merged, a warp to a row
-// (blockIdx.y: every gridDim.y-th of them):
+// CTA x merges the block of rows that starts in share x and goes on in the next ones, if
+// there is one (blockIdx.y: every gridDim.y-th row; a warp to a row):
 //   M = max L_s,  O = sum e^{L_s - M} O_s / sum e^{L_s - M},  LSE = M + ln sum e^{L_s - M}.
+// The forward kernel left the block's place; finding it again from the lengths took longer
+// than the merge.
 template <int D, bool BF16, int QT>
-__global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p, int grid) {
+__global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x + 1;
-  int ctas;
-  long long units, x, xe;
-  UnitAt u;
-  if (!find_share<QT>(p, grid, c, nullptr, lane, ctas, units, x, xe, u)) return;
-  if (u.at == 0 || share_start(units, ctas, c - 1) > x - u.at) return;
-  const long long end = x - u.at + block_units<QT>(p, u.s, u.blk);
-  int last = c;  // the last share with a part of the block
-  while (last + 1 < ctas && share_start(units, ctas, last + 1) < end) ++last;
-  const int a = u.blk * QT * p.tpt, n_tok = min(u.s.n, a + QT * p.tpt) - a;
+  const int c = blockIdx.x;
   griddep_wait();
-  constexpr int PER = D / 32;
+  const int4 at = p.merge[c];
+  const int parts = min(at.w, static_cast<int>(gridDim.x) - c);
+  if (parts < 2) return;
+  const int n_tok = min(min(at.y, QT * p.tpt), p.T - at.x);
+  constexpr int PER = D / 32, U = 4;
   for (int i = blockIdx.y * 8 + warp; i < n_tok * p.G; i += 8 * gridDim.y) {
     const int tok = i / p.G, g = i - tok * p.G;
-    const int t = tok / p.tpt;
+    const int t = QT == 1 ? 0 : tok / p.tpt;
     const int r = t * 128 + (tok - t * p.tpt) * p.G + g;
-    const auto slot = [&](int s) {  // row of part s (0: the share that holds the block's start)
-      return (static_cast<size_t>(2 * (c - 1 + s) + (s == 0 ? 1 : 0)) * QT) * 128 + r;
+    const auto slot = [&](int s) {  // row of part s: the first is its share's second slot
+      return (static_cast<size_t>(2 * (c + s) + (s == 0 ? 1 : 0)) * QT) * 128 + r;
     };
-    const int parts = last - c + 2;
     float M = -INFINITY;
     for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.LSE_part[slot(s)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = warp_max(M);
     float acc[PER] = {}, wsum = 0.f;
     if (M != -INFINITY) {
-      for (int s = 0; s < parts; ++s) {
-        const float L = p.LSE_part[slot(s)];
-        if (L == -INFINITY) continue;  // the row sees none of the share's keys
-        const float w = exp2f((L - M) * 1.4426950408889634f);
-        wsum += w;
-        const float* src = p.O_part + slot(s) * D + lane * PER;
+      for (int s0 = 0; s0 < parts; s0 += U) {
+        float L[U], v[U][PER];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+        for (int k = 0; k < U; ++k) L[k] = s0 + k < parts ? p.LSE_part[slot(s0 + k)] : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          // A part of whose keys the row sees none was not written.
+          if (L[k] != -INFINITY) {
+            const float* src = p.O_part + slot(s0 + k) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(src + e);
+              v[k][e] = f.x;
+              v[k][e + 1] = f.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          if (L[k] == -INFINITY) continue;
+          const float w = exp2f((L[k] - M) * 1.4426950408889634f);
+          wsum += w;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        }
       }
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-    const int row = u.s.row0 + a + tok, head = u.kvh * p.G + g;
+    const int row = at.x + tok, head = at.z * p.G + g;
     uint16_t* dst = p.O + row * p.o_row + head * p.o_head + lane * PER;
 #pragma unroll
     for (int e = 0; e < PER; e += 2)

@@ -9,10 +9,10 @@
 
 namespace fa2 {
 
-template <int D, bool BF16, int QT, bool PAGED>
+template <int D, bool BF16, int QT, bool PAGED, int NQ = 0>
 int launch_seq(const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid, cudaStream_t stream) {
-  using Cfg = SeqCfg<D, QT>;
-  auto kern = fa2_seq_fwd_kernel<D, BF16, QT, PAGED>;
+  using Cfg = SeqCfg<D, QT, NQ>;
+  auto kern = fa2_seq_fwd_kernel<D, BF16, QT, PAGED, NQ>;
   // The kernel re-splits its registers between warpgroups: only sound when every thread
   // was launched with exactly LAUNCH_REGS of them.
   static const bool regs_ok = [&] {
@@ -28,9 +28,8 @@ int launch_seq(const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
   if (cudaGetLastError() != cudaSuccess) return FA2_ERR_CUDA;
   host_count_launches(1);
   if constexpr (PAGED) {
-    if (grid < 2) return FA2_OK;  // nothing is cut
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, QT == 1 ? 2 : 8);
+    cfg.gridDim = dim3(grid, NQ ? 1 : (QT == 1 ? 4 : 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -38,7 +37,7 @@ int launch_seq(const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fa2_seq_merge_kernel<D, BF16, QT>, p, static_cast<int>(grid)) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, fa2_seq_merge_kernel<D, BF16, QT>, p) != cudaSuccess) {
       cudaGetLastError();
       return FA2_ERR_CUDA;
     }
@@ -47,8 +46,13 @@ int launch_seq(const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
   return FA2_OK;
 }
 
+// qt: 2 or 1 query tiles of 128 rows, or (paged, d <= 128) 16 or 32: few rows.
 template <bool PAGED, bool BF16>
 int launch_seq_any(int d, int qt, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid, cudaStream_t s) {
+  if constexpr (PAGED) {
+    if (qt == 16) return d <= 64 ? launch_seq<64, BF16, 1, true, 16>(m, p, dev, grid, s) : launch_seq<128, BF16, 1, true, 16>(m, p, dev, grid, s);
+    if (qt == 32) return d <= 64 ? launch_seq<64, BF16, 1, true, 32>(m, p, dev, grid, s) : launch_seq<128, BF16, 1, true, 32>(m, p, dev, grid, s);
+  }
   switch (seq_tile_dim(d)) {
     case 64:
       return qt == 2 ? launch_seq<64, BF16, 2, PAGED>(m, p, dev, grid, s) : launch_seq<64, BF16, 1, PAGED>(m, p, dev, grid, s);

@@ -22,11 +22,11 @@
 //
 // Roles (384 threads, three warpgroups):
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1 (QT = 1: warps 4-7 idle)
-//   warp 8          producer: Q, K and V tiles by TMA; pages one box each, a lane to a page
+//   warp 8          Q and K tiles by TMA; pages one box each
 //   warp 9          MMA issuer (one thread)
 //   warp 10         scheduler: finds the CTA's next item while the current one runs
-//   warp 11         zeroes V rows that belong to no visible key (a sequence that ends
-//                   inside a tile), so that nothing there, NaN included, reaches P V
+//   warp 11         V tiles by TMA; zeroes the rows that belong to no visible key (a sequence
+//                   that ends inside a tile), so that nothing there, NaN included, reaches P V
 // The CTA runs its items as one stream: the rings of Q, K and V tiles and every barrier's
 // phase go on across items, the first scores of the next item are issued right behind
 // the last P V of this one, and its epilogue overlaps them.
@@ -91,7 +91,7 @@ struct SeqCfg {
 
 enum SeqSite : uint32_t {
   kQSiteItem = 80, kQSiteItemEmpty, kQSiteProd, kQSiteMmaQ, kQSiteMmaK, kQSiteMmaV, kQSiteMmaP, kQSiteMmaO,
-  kQSiteMmaDrain, kQSiteSoftS, kQSiteSoftO, kQSiteFix, kQSiteClc, kQSiteDrain
+  kQSiteMmaDrain, kQSiteSoftS, kQSiteSoftO, kQSiteClc, kQSiteDrain
 };
 
 constexpr int kSeqItems = 4;  // ring of items handed to the roles
@@ -503,7 +503,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     abort_flag = 0;
     for (int i = 0; i < NI; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 3 + (NQ ? 8 : 4 * QT));  // producer, MMA, V fix and the softmax warps
+      mbar_init(&item_empty[i], 3 + (NQ ? 8 : 4 * QT));  // two producers, MMA and the softmax warps
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -623,35 +623,36 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       it.valid = 0;
       if (ok) publish(it);
-    } else if (warp == 8) {
-      // ---------------------------------------------------------------- producer
-      const uint64_t keep = policy_evict_last();
-      int qc = 0, kc = 0, vc = 0;       // tiles loaded
-      unsigned int raw = 0;             // V slots whose last load went to v_raw
-      unsigned int raw_par = 0;         // parity of the loads on v_raw, per slot
-      bool ok = true, skipped = false;  // test hook: the first K tile was not loaded
-      const int nbox = 128 / (PAGED ? p.box_rows : 128);
+    } else if (warp == 8 || warp == 11) {
+      // ---------------------------------------------------------------- producers
+      // Warp 8 loads the Q and K tiles, warp 11 the V tiles, each in the order in which the MMA
+      // issuer takes them.  (A page of 16 positions is 2 KB to a box: one warp issuing the
+      // boxes of both held a decode step to 3.8 TB/s.)  Warp 11 also zeroes the V rows that no
+      // row of the item sees, once such a tile has landed (on v_raw; v_full is then its own).
+      const bool is_v = warp == 11;
+      [[maybe_unused]] const uint64_t keep = policy_evict_last();
+      const CUtensorMap* map = is_v ? &tmV : &tmK;
+      uint8_t* ring = is_v ? sV : sK;
+      const int slots = is_v ? C::VS : C::KS;
+      uint64_t* full = is_v ? v_full : k_full;
+      uint64_t* empty = is_v ? v_empty : k_empty;
+      int qc = 0, slot = 0;              // Q tiles loaded; this warp's next slot
+      unsigned int turn = 0;             // parity of the turn around the ring
+      bool round = false;                // the ring has been around once
+      unsigned int raw_par = 0;          // V: parity of the loads on v_raw, per slot
+      int fix = -1, fix_a = 0, fix_e = 0;  // V: slot to be zeroed outside rows [fix_a, fix_e)
+      bool ok = true, skip = p.fault == 1 && !is_v;  // test hook: the first K tile is not loaded
+      [[maybe_unused]] const int nbox = PAGED ? 128 / p.box_rows : 1;
       auto wait_all = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, mbar_wait_far(bar, par, wc, kQSiteProd)) != 0;
       };
-      auto load_q = [&](const SeqItem& it, int t) -> bool {
-        const int s = qc % C::QS;
-        if (qc >= C::QS && !wait_all(&q_empty[s], ((qc / C::QS) - 1) & 1)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[s], C::KCH * 128 * p.G * p.tpt);
-          for (int c = 0; c < C::KCH; ++c)
-            tma_load_3d(sQ + s * C::QTILE + c * C::QCHUNK, &tmQ, &q_full[s], c * 64, it.kvh * p.G,
-                        it.row0 + t * p.tpt);
-        }
-        ++qc;
-        return true;
-      };
-      // Lane i: the page of box i of tile j (read ahead of the tile's loads).
+      // Lane i: the page of box i of tile j (read a tile ahead of its loads).
       auto pages_of = [&](const SeqItem& it, int j) -> int {
         int a, e, pg = 0;
         tile_keys(it, j, a, e);
         if (lane < nbox && lane * p.box_rows < e && (lane + 1) * p.box_rows > a) {
-          pg = p.block_table[static_cast<size_t>(it.key0) * p.max_blocks + (j * 128 + lane * p.box_rows) / p.block_size];
+          const int at = p.block_size <= 128 ? j * nbox + lane : j * 128 / p.block_size;
+          pg = p.block_table[static_cast<size_t>(it.key0) * p.max_blocks + at];
           if (pg < 0 || pg >= p.num_blocks) {
             atomicCAS(p.status, 0u, kStatusInvalid | (kPSiteBlock << 8));
             pg = p.num_blocks;  // outside the map: reads as zeros
@@ -659,7 +660,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         return pg;
       };
-      auto load_tile = [&](const SeqItem& it, int j, int pg, const CUtensorMap* map, uint8_t* dst, uint64_t* bar) {
+      auto load_tile = [&](const SeqItem& it, int j, int pg, uint8_t* dst, uint64_t* bar) {
         if constexpr (!PAGED) {
           if (lane == 0) {
             mbar_arrive_expect_tx(bar, C::TILE);
@@ -670,39 +671,34 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           int a, e;
           tile_keys(it, j, a, e);
           const int i0 = a / p.box_rows, n = (e + p.box_rows - 1) / p.box_rows - i0;
+          const int row = p.block_size <= 128 ? 0 : j * 128 % p.block_size;
           if (lane == 0) mbar_arrive_expect_tx(bar, n * p.box_rows * 128 * C::KCH);
           __syncwarp();
-          for (int x0 = 0; x0 < n * C::KCH; x0 += 32) {
-            const int x = x0 + lane, i = i0 + x / C::KCH, c = x % C::KCH;
-            const int page = __shfl_sync(0xffffffffu, pg, i & 31);
-            if (x < n * C::KCH)
-              tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64,
-                          (j * 128 + i * p.box_rows) % p.block_size, it.kvh, page);
+#pragma unroll 1
+          for (int i = i0; i < i0 + n; ++i) {
+            const int page = __shfl_sync(0xffffffffu, pg, i);
+            if (lane == 0) {
+#pragma unroll
+              for (int c = 0; c < C::KCH; ++c)
+                tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64, row, it.kvh, page);
+            }
           }
         }
       };
-      auto load_k = [&](const SeqItem& it, int j, int pg) -> bool {
-        const int s = kc % C::KS;
-        if (kc >= C::KS && !wait_all(&k_empty[s], ((kc / C::KS) - 1) & 1)) return false;
-        if (p.fault == 1 && kc == 0) skipped = true;
-        else load_tile(it, j, pg, &tmK, sK + s * C::TILE, &k_full[s]);
-        ++kc;
+      auto zero_rows = [&]() -> bool {
+        if (!wait_all(&v_raw[fix], raw_par >> fix & 1)) return false;
+        raw_par ^= 1u << fix;
+        uint8_t* v = sV + fix * C::TILE + (lane & 7) * 16;
+        for (int r = lane >> 3; r < 128; r += 4)
+          if (r < fix_a || r >= fix_e)
+            for (int c = 0; c < C::KCH; ++c)
+              *reinterpret_cast<uint4*>(v + c * C::CHUNK + r * 128) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[fix]);
+        fix = -1;
         return true;
       };
-      auto load_v = [&](const SeqItem& it, int j, int pg) -> bool {
-        const int s = vc % C::VS;
-        if (vc >= C::VS && !wait_all(&v_empty[s], ((vc / C::VS) - 1) & 1)) return false;
-        int a, e;
-        tile_keys(it, j, a, e);
-        const bool fix = a > 0 || e < 128;
-        load_tile(it, j, pg, &tmV, sV + s * C::TILE, fix ? &v_raw[s] : &v_full[s]);
-        raw = fix ? raw | (1u << s) : raw & ~(1u << s);
-        if (fix) raw_par ^= 1u << s;
-        ++vc;
-        return true;
-      };
-      SeqItem old{};  // QT = 1: the tile whose V is still to be loaded, behind the next K
-      int old_j = -1, old_pg = 0;
       for (int ii = 0; ok; ++ii) {
         if (!(ok = wait_all(&item_full[ii % NI], (ii / NI) & 1))) break;
         const SeqItem it = items[ii % NI];
@@ -710,67 +706,57 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (lane == 0) mbar_arrive(&item_empty[ii % NI]);
         if (!it.valid) break;
         if (it.n == 0) continue;
-        int pg = PAGED ? pages_of(it, it.j0) : 0;
-        if (it.hi[0] > 0) ok = load_q(it, 0);
+        int pg = 0;
+        if constexpr (PAGED) pg = pages_of(it, it.j0);
         for (int jj = 0; jj < it.n && ok; ++jj) {
           const int j = it.j0 + jj;
-          const int pg_next = PAGED && jj + 1 < it.n ? pages_of(it, j + 1) : 0;
-          ok = load_k(it, j, pg);
-          if (QT == 2 || NQ) {
-            if (QT == 2 && ok && jj == 0 && it.hi[1] > 0) ok = load_q(it, 1);
-            ok = ok && load_v(it, j, pg);
-          } else {
-            if (ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
-            old = it;
-            old_j = j;
-            old_pg = pg;
+          // Q: tile 0 ahead of the item's first K tile, tile 1 behind it.
+          auto load_q = [&](int t) -> bool {
+            const int s = qc % C::QS;
+            if (qc >= C::QS && !wait_all(&q_empty[s], ((qc / C::QS) - 1) & 1)) return false;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full[s], C::KCH * 128 * p.G * p.tpt);
+              for (int c = 0; c < C::KCH; ++c)
+                tma_load_3d(sQ + s * C::QTILE + c * C::QCHUNK, &tmQ, &q_full[s], c * 64, it.kvh * p.G,
+                            it.row0 + t * p.tpt);
+            }
+            ++qc;
+            return true;
+          };
+          if (!is_v && jj == 0 && it.hi[0] > 0 && !(ok = load_q(0))) break;
+          int pg_next = 0;
+          if constexpr (PAGED) {
+            if (jj + 1 < it.n) pg_next = pages_of(it, j + 1);
           }
+          int a, e;
+          tile_keys(it, j, a, e);
+          const bool part = is_v && (a > 0 || e < 128);
+          // A tile to be zeroed waits until the next load is out, or has no slot yet.
+          if (fix >= 0 && (part || (round && !__all_sync(0xffffffffu, mbar_test(&empty[slot], turn ^ 1)))))
+            if (!(ok = zero_rows())) break;
+          if (round && !(ok = wait_all(&empty[slot], turn ^ 1))) break;
+          if (!skip) load_tile(it, j, pg, ring + slot * C::TILE, part ? &v_raw[slot] : &full[slot]);
+          skip = false;
+          if (fix >= 0 && !(ok = zero_rows())) break;
+          if (part) fix = slot, fix_a = a, fix_e = e;
+          if (++slot == slots) slot = 0, turn ^= 1, round = true;
+          if (QT == 2 && !is_v && jj == 0 && it.hi[1] > 0) ok = load_q(1);
           pg = pg_next;
         }
       }
-      if (QT == 1 && !NQ && ok && old_j >= 0) ok = load_v(old, old_j, old_pg);
+      if (ok && fix >= 0) ok = zero_rows();
       if (lane == 0) {
         // Every copy that was issued lands before the CTA leaves, on a timeout too.
         volatile int no_abort = 0;
         WaitCtl dw{p.status, &no_abort, 100000000ull};
-        for (int i = max(0, qc - C::QS); i < qc; ++i) mbar_wait_far(&q_full[i % C::QS], (i / C::QS) & 1, dw, kQSiteDrain);
-        for (int i = max(0, kc - C::KS); i < kc; ++i)
-          if (!(skipped && i == 0)) mbar_wait_far(&k_full[i % C::KS], (i / C::KS) & 1, dw, kQSiteDrain);
-        for (int i = max(0, vc - C::VS); i < vc; ++i) {
-          const int s = i % C::VS;
-          if (raw >> s & 1) mbar_wait_far(&v_raw[s], (raw_par >> s & 1) ^ 1, dw, kQSiteDrain);
-          else mbar_wait_far(&v_full[s], (i / C::VS) & 1, dw, kQSiteDrain);
-        }
-      }
-      __syncwarp();
-    } else if (warp == 11) {
-      // ---------------------------------------------------------------- V rows of no visible key
-      int vc = 0;
-      unsigned int par = 0;
-      bool ok = true;
-      for (int ii = 0; ok; ++ii) {
-        ok = __all_sync(0xffffffffu, mbar_wait_far(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem));
-        if (!ok) break;
-        const SeqItem it = items[ii % NI];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&item_empty[ii % NI]);
-        if (!it.valid) break;
-        for (int jj = 0; jj < it.n && ok; ++jj, ++vc) {
-          int a, e;
-          tile_keys(it, it.j0 + jj, a, e);
-          if (a <= 0 && e >= 128) continue;
-          const int s = vc % C::VS;
-          ok = __all_sync(0xffffffffu, mbar_wait_far(&v_raw[s], par >> s & 1, wc, kQSiteFix));
-          if (!ok) break;
-          par ^= 1u << s;
-          uint8_t* v = sV + s * C::TILE + (lane & 7) * 16;
-          for (int r = lane >> 3; r < 128; r += 4)
-            if (r < a || r >= e)
-              for (int c = 0; c < C::KCH; ++c)
-                *reinterpret_cast<uint4*>(v + c * C::CHUNK + r * 128) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[s]);
+        for (int i = max(0, qc - C::QS); i < qc; ++i)
+          mbar_wait_far(&q_full[i % C::QS], (i / C::QS) & 1, dw, kQSiteDrain);
+        if (fix >= 0) mbar_wait_far(&v_raw[fix], raw_par >> fix & 1, dw, kQSiteDrain);
+        for (int i = 0; i < slots; ++i) {
+          // Slots before `slot` were last loaded in this turn, the others in the one before.
+          const bool now = i < slot;
+          if ((!now && !round) || i == fix || (p.fault == 1 && !is_v && !round && i == 0)) continue;
+          mbar_wait_far(&full[i], now ? turn : turn ^ 1, dw, kQSiteDrain);
         }
       }
       __syncwarp();

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfa2.so")
 BUILD = os.path.join(HERE, "_build")  # object files
 SOURCES = [os.path.join(CSRC, f) for f in (
-    "fa2_api.cu", "fa2_seq_api.cu", "fa2_seq_packed.cu", "fa2_seq_paged.cu")]
+    "fa2_api.cu", "fa2_seq_api.cu", "fa2_seq_packed.cu", "fa2_seq_paged.cu",
+    "fa2_seq_bwd.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", "fa2.h")]
 DEPS = SOURCES + HEADERS

@@ -24,7 +24,7 @@ constexpr int kMaxGroup = 128;  // query heads to a key/value head: rows of one 
 
 int check_sizes(int B, int T, int H, int Hkv, int d, int max_d) {
   if (B < 1 || T < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || H / Hkv > kMaxGroup) return FA2_ERR_INVALID_ARG;
-  if (B > (1 << 24) || T > (1 << 30) || H > 65535) return FA2_ERR_INVALID_ARG;
+  if (B > (1 << 24) || T > (1 << 30) || H > 32767) return FA2_ERR_INVALID_ARG;
   if (d < 8 || d > max_d || d % 8 != 0) return FA2_ERR_UNSUPPORTED;
   return FA2_OK;
 }
@@ -53,6 +53,18 @@ bool cache_ok(const fa2_cache* x, int blocks, int heads, int rows, int d) {
 // Sequences that may hold a partial block: the empty ones too where the order of the blocks
 // keeps a place for each (BlockOrder).
 int partial_blocks(int B, int T, int held) { return B > held ? B : std::min(B, T); }
+
+// Key/value heads to a group of the item order: as many equal groups as leave each `waves`
+// waves of items.  Fewer leave SMs without work where a group's longest items start last,
+// more let the heads' rows fall out of L2.  Measured on B200 (heads to a group): backward of
+// 14k tokens, d = 128, 890 items of very different length: 1: 1762, 3: 1727, 4: 1620, 8: 1570
+// us, of 8 x 4096 tokens, 4200 items: 3: 1900, 5: 2012 us; forward of 15k tokens, d = 64,
+// 1050 items: 1: 177, 3: 162, 8: 142 us, of 22k tokens, d = 128, 2800 items: 1: 1258, 4: 1214,
+// 8: 1226 us.
+int head_group(long long items, int waves, int Hkv, int n_sm) {
+  const long long groups = std::min<long long>(Hkv, std::max(1ll, items / (static_cast<long long>(waves) * n_sm)));
+  return static_cast<int>((Hkv + groups - 1) / groups);
+}
 
 // ---- forward over packed sequences and paged caches ----
 
@@ -125,50 +137,25 @@ size_t paged_bytes(int grid, int qt, int d) {
 
 // ---- backward ----
 
+constexpr long long kBwdWaves = 3;
+
 int bwd_tile_dim(int d) { return d <= 64 ? 64 : 128; }
 
 // Query tiles of one key/value head: each sequence's last one may be partial.
 long long bwd_tiles(int B, int T, int G) { return T / (128 / G) + static_cast<long long>(B); }
 
+// Work items of the backward, and the parts that a key tile's query tiles are cut into: as
+// many as give about three waves of items on a B200's 148 SMs, eight at most.
+long long bwd_items(int B, int T, int Hkv) {
+  return (T / 128 + static_cast<long long>(partial_blocks(B, T, fa2::kHeldBwd))) * Hkv;
+}
+int bwd_split(int B, int T, int Hkv) {
+  return static_cast<int>(std::min(8ll, std::max(1ll, kBwdWaves * 148 / std::max(1ll, bwd_items(B, T, Hkv)))));
+}
+
 // Workspace: D and LSE * log2 e per row, then the float dQ accumulator.
 size_t bwd_stat_bytes(int B, int T, int H, int Hkv) {
   return static_cast<size_t>(bwd_tiles(B, T, H / Hkv)) * Hkv * 128 * 4;  // a multiple of 512
-}
-
-template <typename... KArgs, typename... Args>
-bool launch_chained(void (*kern)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
-  // Programmatic serialisation: the kernel may be set up while the one before it on the
-  // stream finishes, and waits on the device before it reads.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess) {
-    fa2::host_count_launches(1);
-    return true;
-  }
-  cudaGetLastError();
-  return false;
-}
-
-template <int D, bool BF16>
-int launch_seq_bwd(const CUtensorMap (&m)[5], const fa2::SeqBwdParams& p, int dev, unsigned int items, cudaStream_t s) {
-  using Cfg = fa2::SeqBwdCfg<D>;
-  auto kern = fa2::fa2_seq_bwd_kernel<D, BF16>;
-  static std::atomic<bool> smem_set[fa2::kSeqDevices];
-  if (!fa2::seq_smem_once(kern, dev, Cfg::SMEM, smem_set)) return FA2_ERR_CUDA;
-  const dim3 rows(static_cast<unsigned int>(p.tiles) * (128 * D / 8 / 256), p.Hkv);
-  if (!launch_chained(fa2::fa2_seq_bwd_pre_kernel<D, BF16>, rows, 256, 0, s, p) ||
-      !launch_chained(kern, dim3(items), Cfg::THREADS, Cfg::SMEM, s, m[0], m[1], m[2], m[3], m[4], p) ||
-      !launch_chained(fa2::fa2_seq_bwd_dq_kernel<D, BF16>, rows, 256, 0, s, p))
-    return FA2_ERR_CUDA;
-  return FA2_OK;
 }
 
 }  // namespace
@@ -205,8 +192,7 @@ int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
       !map_packed(&m.v, V, T, Hkv, d, dtype, true, 128, 1))
     return FA2_ERR_CUDA;
   fa2::SeqParams p = seq_params(O, LSE, cu_seqlens, st, B, T, H, Hkv, d, scale, causal, window);
-  const long long per_head = items(qt) / Hkv;
-  p.head_group = static_cast<int>(std::min<long long>(Hkv, std::max<long long>(1, (2LL * n_sm + per_head - 1) / per_head)));
+  p.head_group = head_group(items(qt), 6, Hkv, n_sm);
   return fa2::launch_seq_packed(d, dtype == FA2_BF16, qt, m, p, dev, static_cast<unsigned int>(items(qt)),
                                 reinterpret_cast<cudaStream_t>(stream));
 }
@@ -214,7 +200,9 @@ int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
 size_t fa2_bwd_varlen_workspace_size(int B, int T, int H, int Hkv, int d) {
   if (check_sizes(B, T, H, Hkv, d, kMaxBwdHeadDim) != FA2_OK) return 0;
   const size_t rows = static_cast<size_t>(bwd_tiles(B, T, H / Hkv)) * Hkv * 128;
-  return 2 * bwd_stat_bytes(B, T, H, Hkv) + rows * bwd_tile_dim(d) * 4;
+  const int split = bwd_split(B, T, Hkv);
+  const size_t part = split > 1 ? static_cast<size_t>(split) * 2 * T * Hkv * bwd_tile_dim(d) * 4 : 0;
+  return (2 * bwd_stat_bytes(B, T, H, Hkv) + rows * bwd_tile_dim(d) * 4 + part + 255) / 256 * 256;
 }
 
 int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V,
@@ -245,8 +233,8 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   if (rc != FA2_OK) return rc;
   const int G = H / Hkv, tpt = 128 / G, D = bwd_tile_dim(d);
   const long long tiles = bwd_tiles(B, T, G);
-  const long long items = (T / 128 + static_cast<long long>(partial_blocks(B, T, fa2::kHeldBwd))) * Hkv;
-  if (tiles * 128 > 0x7fffffffll || items > 0x7fffffffll) return FA2_ERR_INVALID_ARG;
+  const long long items = bwd_items(B, T, Hkv);
+  if (tiles * 128 > 0x7fffffffll || items > (0x7fffffffll >> 3)) return FA2_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t stat = bwd_stat_bytes(B, T, H, Hkv);
   fa2::SeqBwdParams p{};
@@ -259,6 +247,8 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   p.Dg = reinterpret_cast<float*>(ws);
   p.Lg = reinterpret_cast<float*>(ws + stat);
   p.acc = reinterpret_cast<float*>(ws + 2 * stat);
+  p.kv_part = p.acc + static_cast<size_t>(tiles) * Hkv * 128 * D;
+  p.split = bwd_split(B, T, Hkv);
   p.cu = cu_seqlens;
   p.status = st;
   p.wait_ns = fa2::host_wait_ns();
@@ -266,12 +256,7 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
   p.B = B, p.T = T, p.Hkv = Hkv, p.G = G, p.d = d, p.tpt = tpt, p.tiles = static_cast<int>(tiles);
   p.causal = causal, p.window = std::min(window, T);  // no row sees more than T keys
   p.scale = scale, p.scale_log2 = scale * 1.4426950408889634f;
-  // Heads to a group of the item order: at least two waves of items, and about 192 MB of the
-  // heads' rows (K, V, G times Q, dO and the float dQ), so that they stay in L2.
-  const long long per_item_head = std::max<long long>(1, items / Hkv);
-  const long long per_head = static_cast<long long>(T) * D * (4 + 8 * G);
-  const long long hg = std::max((2LL * n_sm + per_item_head - 1) / per_item_head, (192LL << 20) / std::max<long long>(1, per_head));
-  p.head_group = static_cast<int>(std::min<long long>(Hkv, std::max<long long>(1, hg)));
+  p.head_group = head_group(items, 4, Hkv, n_sm);
   CUtensorMap m[5];
   const uint64_t adims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(tiles) * 128, static_cast<uint64_t>(Hkv)};
   const uint64_t astr[2] = {static_cast<uint64_t>(D) * 4, static_cast<uint64_t>(tiles) * 128 * D * 4};
@@ -281,10 +266,8 @@ int fa2_bwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V
       !fa2::host_encode_map(&m[4], fa2::MapType::kF32, p.acc, 3, adims, astr, abox))
     return FA2_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned int n = static_cast<unsigned int>(items);
-  if (D == 64)
-    return dtype == FA2_BF16 ? launch_seq_bwd<64, true>(m, p, dev, n, s) : launch_seq_bwd<64, false>(m, p, dev, n, s);
-  return dtype == FA2_BF16 ? launch_seq_bwd<128, true>(m, p, dev, n, s) : launch_seq_bwd<128, false>(m, p, dev, n, s);
+  const unsigned int n = static_cast<unsigned int>(items * p.split);
+  return fa2::launch_seq_bwd(D, dtype == FA2_BF16, m, p, dev, n, s);
 }
 
 size_t fa2_fwd_paged_workspace_size(int B, int T, int H, int Hkv, int d, int sm_count) {

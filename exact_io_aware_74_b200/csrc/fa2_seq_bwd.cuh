@@ -18,9 +18,13 @@
 //     shared memory by a warp of its own before any product reads them: a product with
 //     a zero weight would still pass on a NaN of the neighbouring sequence.
 //
+// Where the items are too few for the SMs, the query tiles of each key tile are cut into
+// `split` parts, one item each: dK and dV then go to the workspace as float parts, which
+// the last kernel sums in order (repeatable all the same).
+//
 // Kernels per call, chained by programmatic dependent launch: fa2_seq_bwd_pre_kernel
 // (D, LSE log2 e, zeroed accumulator), fa2_seq_bwd_kernel, fa2_seq_bwd_dq_kernel
-// (dQ = scale * accumulator, to 16 bits and to its place).
+// (dQ = scale * accumulator, to 16 bits and to its place; split dK and dV).
 #pragma once
 
 #include <cstdint>
@@ -37,13 +41,27 @@ struct SeqBwdParams {
   const float* LSE;  // [H][T]
   float *Dg, *Lg;    // [Hkv][tiles * 128]
   float* acc;        // [Hkv][tiles * 128][D]
+  float* kv_part;    // split > 1: [split][dV, dK][T][Hkv][D]
   const int* cu;
   unsigned int* status;
   unsigned long long wait_ns;
   int B, T, Hkv, G, d, tpt, tiles;  // tiles: query tiles of one key/value head, room included
   int causal, window, fault, head_group;
+  int split;         // parts that a key tile's query tiles are cut into
   float scale, scale_log2;
 };
+
+// Query tiles [i0, i0 + n) that see key tile j of a sequence of len rows.
+__device__ __forceinline__ void query_range(const SeqBwdParams& p, int len, int j, int& i0, int& n) {
+  const int n_q = (len + p.tpt - 1) / p.tpt;
+  i0 = p.causal ? j * 128 / p.tpt : 0;
+  int e = n_q;
+  if (p.window > 0) {
+    const long long t = static_cast<long long>(j) * 128 + 127 + p.window - 1;  // last token that sees the tile
+    e = static_cast<int>(min(static_cast<long long>(n_q), t / p.tpt + 1));
+  }
+  n = e - i0;
+}
 
 // First query tile of sequence b.
 __device__ __forceinline__ int tile_base(const SeqBwdParams& p, int b) {
@@ -114,7 +132,40 @@ __global__ void __launch_bounds__(256) fa2_seq_bwd_dq_kernel(const SeqBwdParams 
   constexpr int TPR = D / 8, RPB = 256 / TPR;
   griddep_wait();
   const int sub = threadIdx.x % TPR;
-  const int r = blockIdx.x * RPB + threadIdx.x / TPR, hk = blockIdx.y;
+  const int r = blockIdx.x * RPB + threadIdx.x / TPR;
+  if (static_cast<int>(blockIdx.y) >= p.Hkv) {
+    // Split key tiles: dV and dK of packed row r, the parts summed in order.
+    if (r >= p.T || sub * 8 >= p.d) return;
+    const int hk = blockIdx.y - p.Hkv;
+    int i = 0, j = p.B;  // the sequence of row r
+    while (j - i > 1) {
+      const int m = (i + j) >> 1;
+      if (p.cu[m] <= r) i = m; else j = m;
+    }
+    const int key = r - min(max(p.cu[i], 0), p.T), len = rows_of(p.cu, p.T, i);
+    if (key < 0 || key >= len) return;
+    int i0, n;
+    query_range(p, len, key >> 7, i0, n);
+    const int parts = min(p.split, n);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float a[8] = {};
+      for (int k = 0; k < parts; ++k) {
+        const float4* s = reinterpret_cast<const float4*>(
+            p.kv_part + (((static_cast<size_t>(k) * 2 + w) * p.T + r) * p.Hkv + hk) * D + sub * 8);
+        const float4 x = s[0], y = s[1];
+        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+      }
+      const float f = w ? p.scale : 1.0f;
+      uint16_t* dst = w ? p.dK + r * p.dk_row + hk * p.dk_head : p.dV + r * p.dv_row + hk * p.dv_head;
+      *reinterpret_cast<uint4*>(dst + sub * 8) =
+          make_uint4(pack2<BF16>(a[0] * f, a[1] * f), pack2<BF16>(a[2] * f, a[3] * f), pack2<BF16>(a[4] * f, a[5] * f),
+                     pack2<BF16>(a[6] * f, a[7] * f));
+    }
+    return;
+  }
+  const int hk = blockIdx.y;
   int row, g;
   if (!row_of(p, r, row, g) || sub * 8 >= p.d) return;
   const float4* s = reinterpret_cast<const float4*>(p.acc + (static_cast<size_t>(hk) * p.tiles * 128 + r) * D + sub * 8);
@@ -134,6 +185,7 @@ struct SeqBwdItem {
   int kvh, j;      // key/value head, key tile
   int i0, n_it;    // query tiles i0 .. i0 + n_it - 1
   int qt0, valid;  // the sequence's first query tile in the workspace
+  int part, pad;   // SPLIT: which part of the key tile's query tiles
 };
 
 template <int D_>
@@ -182,7 +234,7 @@ enum SeqBwdSite : uint32_t {
   kRSiteCmpDQ, kRSiteDrain
 };
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
 fa2_seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -273,23 +325,24 @@ fa2_seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     int w = blockIdx.x;
     BlockAt at;
     for (int k = 0; ok && w >= 0; ++k) {
-      if (order.find(p.cu, p.B, p.T, p.Hkv, p.head_group, 128, w, lane, at)) {
+      const int ws = SPLIT ? w / p.split : w;
+      [[maybe_unused]] const int s = SPLIT ? w - ws * p.split : 0;
+      if (order.find(p.cu, p.B, p.T, p.Hkv, p.head_group, 128, ws, lane, at)) {
         it.row0 = min(max(p.cu[at.b], 0), p.T);
         it.n = rows_of(p.cu, p.T, at.b);
         it.kvh = at.kvh;
         // Causal: key tile 0 has the most query tiles.
         it.j = (it.n + 127) / 128 - 1 - at.level;
-        const int n_q = (it.n + tpt - 1) / tpt;
-        it.i0 = p.causal ? it.j * 128 / tpt : 0;
-        int e = n_q;
-        if (p.window > 0) {
-          const long long t = static_cast<long long>(it.j) * 128 + 127 + p.window - 1;  // last token that sees the tile
-          e = static_cast<int>(min(static_cast<long long>(n_q), t / tpt + 1));
+        query_range(p, it.n, it.j, it.i0, it.n_it);
+        if constexpr (SPLIT) {  // part s of at most `split`
+          const int parts = min(p.split, it.n_it), a = it.n_it * s / parts, e = it.n_it * (s + 1) / parts;
+          it.part = s;
+          it.i0 += a;
+          it.n_it = s < parts ? e - a : 0;
         }
-        it.n_it = e - it.i0;
         it.qt0 = tile_base(p, at.b);
         it.valid = 1;
-        ok = publish();
+        if (it.n_it > 0) ok = publish();
       }
       // The next index only once the item before this one is done with.
       if (ok && ii >= 2)
@@ -786,8 +839,16 @@ fa2_seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int f = 0; f < 4; ++f)
             w[f] = pack2<BF16>(__uint_as_float(rr[8 * e + 2 * f]) * mul, __uint_as_float(rr[8 * e + 2 * f + 1]) * mul);
-          if (key < it.n && c * 32 + 8 * e < p.d)
+          if (!SPLIT && key < it.n && c * 32 + 8 * e < p.d)
             *reinterpret_cast<uint4*>(row + c * 32 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (SPLIT && key < it.n) {
+          float4* dst = reinterpret_cast<float4*>(
+              p.kv_part + (((static_cast<size_t>(it.part) * 2 + g) * p.T + it.row0 + key) * p.Hkv + it.kvh) * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(rr[4 * e]), __uint_as_float(rr[4 * e + 1]),
+                                 __uint_as_float(rr[4 * e + 2]), __uint_as_float(rr[4 * e + 3]));
         }
       }
     }

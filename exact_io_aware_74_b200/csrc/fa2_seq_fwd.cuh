@@ -173,14 +173,18 @@ __device__ __forceinline__ void cut_item(SeqItem& it, int a, int e) {
   it.n = max(it.hi[0], it.hi[1]) - it.j0;
 }
 
-// Units of work of block blk of a sequence: its key tiles (both query tiles' together),
-// at least one.
+// Units of work of block blk of a sequence: its key tiles (both query tiles' together, at
+// least one) and kItemUnits for its start and end, which come first in the linear order.
+// (An item of two query tiles costs about 5 us beside 2.6 us a key tile.  With key tiles
+// alone the share with a prompt's many short blocks ended at 300 us, the others at 175.)
+template <int QT>
+constexpr int kItemUnits = QT == 2 ? 2 : 1;
 template <int QT>
 __device__ __forceinline__ int block_units(const SeqParams& p, int n, int nk, int blk) {
   const int a = blk * (QT * p.tpt);
   int lo, hi;
   key_range(p, SeqLen{0, n, nk}, a, min(n, a + QT * p.tpt), lo, hi);
-  return max(1, hi - lo);
+  return max(1, hi - lo) + kItemUnits<QT>;
 }
 __device__ __forceinline__ int blocks_of(int n, int R) { return n <= R ? (n > 0) : (n + R - 1) / R; }
 
@@ -568,17 +572,22 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const int len = block_units<QT>(p, u.s.n, u.s.nk, u.blk);
             const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
             make_item<true, QT>(p, u.s, u.b, u.kvh, u.blk, it);
-            if (u.at > 0 || take < len) {
-              if (u.at == 0 && lane == 0) {
-                // The block starts here and goes on in the next shares: for the merge kernel.
-                int parts = 1;
-                for (long long e = xe; e < x + len; e += per) ++parts;
-                p.merge[c] = make_int4(it.row0, it.n_tok, u.kvh, parts);
+            // Key tiles [a, e) of the block's fall into this share.
+            constexpr int C0 = kItemUnits<QT>;
+            const int a = max(0, u.at - C0), e = max(0, u.at + take - C0);
+            if (e > a) {
+              if (a > 0 || e < len - C0) {
+                if (a == 0 && lane == 0) {
+                  // The block goes on in the next shares: for the merge kernel.
+                  int parts = 1;
+                  for (long long end = xe; end < x + len - u.at; end += per) ++parts;
+                  p.merge[c] = make_int4(it.row0, it.n_tok, u.kvh, parts);
+                }
+                cut_item(it, a, e);
+                it.part = 2 * c + (a > 0 ? 0 : 1);
               }
-              cut_item(it, u.at, u.at + take);
-              it.part = 2 * c + (u.at > 0 ? 0 : 1);
+              ok = publish(it);
             }
-            ok = publish(it);
             x += take;
             if (x >= xe) break;
             u.at = 0;

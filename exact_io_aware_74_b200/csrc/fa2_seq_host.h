@@ -1,4 +1,4 @@
-// Launches of the packed and paged forward kernels, one translation unit each.
+// Launches of the packed and paged kernels, one translation unit each.
 #pragma once
 
 #include <cuda.h>
@@ -22,6 +22,12 @@ int launch_seq_packed(int d, bool bf16, int qt, const SeqMaps& m, const SeqParam
                       cudaStream_t s);
 int launch_seq_paged(int d, bool bf16, int qt, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
                      cudaStream_t s);
+
+struct SeqBwdParams;
+
+// D: tile width (64 or 128); maps: Q, K, V, dO, dQ accumulator.
+int launch_seq_bwd(int D, bool bf16, const CUtensorMap (&maps)[5], const SeqBwdParams& p, int dev, unsigned int items,
+                   cudaStream_t s);
 
 // Raises a kernel's dynamic shared memory limit once per device; every kernel passes flags
 // of its own.

@@ -71,12 +71,16 @@ struct SeqCfg {
   // Ring stages within 227 KB (tiles of 16, 32, 48, 64 KB).  Two query tiles have a third
   // slot at D = 128, so that the next item's first tile loads during this one.
   static constexpr int QS = NQ ? 2 : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 3 : 2) : 1));
-  static constexpr int KS = NQ ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : (D == 256 ? 1 : 2));
-  static constexpr int VS = NQ ? KS : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1));
-  // Few rows: P^T of each warpgroup, two chunks of 64 keys.  (At D = 64 the V operand's
+  // (Few rows: as many S blocks as K slots; V slots in even number, see the issuer.)
+  static constexpr int KS = NQ ? (D == 64 ? 6 : 4) : (D == 64 ? 4 : (D == 256 ? 1 : 2));
+  static constexpr int VS = NQ ? (D == 64 ? 6 : 2) : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1));
+  // Few rows: P^T of each warpgroup, two chunks of 64 keys, PB buffers each (with two a
+  // warpgroup need not wait for its last product before it writes the next P).  (At D = 64 the V operand's
   // upper 64 rows are whatever lies 16 KB behind the tile: at least that much follows.)
-  static constexpr int PBUF = 2 * NQ * 128;
-  static constexpr int REST = NQ ? (QS * QTILE + 2 * PBUF < CHUNK ? CHUNK : QS * QTILE + 2 * PBUF) : QS * TILE;
+  static constexpr int PBUF = 2 * NQ * 128, PB = NQ == 16 && D == 64 ? 2 : 1;
+  static_assert(NQ == 0 || (VS % 2 == 0 && 2 * PB <= VS), "a product's barrier comes round after its P buffer");
+  static constexpr int PREST = QS * QTILE + 2 * PB * PBUF;
+  static constexpr int REST = NQ ? (PREST < CHUNK ? CHUNK : PREST) : QS * TILE;
   static constexpr int SMEM = (KS + VS) * TILE + REST + 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory");
   static constexpr int THREADS = 384;
@@ -492,7 +496,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __shared__ uint64_t item_full[NI], item_empty[NI], clc_full;
   __shared__ uint64_t q_full[C::QS], q_empty[C::QS], k_full[C::KS], k_empty[C::KS];
   __shared__ uint64_t v_full[C::VS], v_empty[C::VS], v_raw[C::VS];
-  __shared__ uint64_t s_full[4], s_free[4], p_ready[2], o_done[2], o_free[2], drain;
+  __shared__ uint64_t s_full[6], s_free[2], p_ready[4], o_done[6], o_free[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int held[kHeld];  // the scheduling warp's
@@ -509,13 +513,13 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], 3 + (NQ ? 8 : 4 * QT));  // two producers, MMA and the softmax warps
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_ready[i], 4);
       mbar_init(&o_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&p_ready[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_free[i], 4);
       mbar_init(&o_free[i], NQ ? 8 : 4);
     }
     mbar_init(&clc_full, 1);
@@ -575,7 +579,17 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // Key tiles [a, e) of the block's fall into this share.
             constexpr int C0 = kItemUnits<QT>;
             const int a = max(0, u.at - C0), e = max(0, u.at + take - C0);
-            if (e > a) {
+            if (it.n == 0) {
+              // Rows that see no key: O = 0 and LSE = -inf, here.  (The other roles then never
+              // meet an item without key tiles, which would be in the way of the next one.)
+              if (e > a)
+                for (int r = 0; r < it.n_tok * p.G; ++r) {
+                  const int row = it.row0 + r / p.G, head = u.kvh * p.G + r % p.G;
+                  if (lane * 8 < p.d)
+                    *reinterpret_cast<uint4*>(p.O + row * p.o_row + head * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
+                  if (lane == 0) p.LSE[static_cast<size_t>(head) * p.T + row] = -INFINITY;
+                }
+            } else if (e > a) {
               if (a > 0 || e < len - C0) {
                 if (a == 0 && lane == 0) {
                   // The block goes on in the next shares: for the merge kernel.
@@ -644,7 +658,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       uint8_t* ring = is_v ? sV : sK;
       const int slots = is_v ? C::VS : C::KS;
       uint64_t* full = is_v ? v_full : k_full;
-      uint64_t* empty = is_v ? v_empty : k_empty;
+      // Few rows: a product's completion barrier is its slot's release too.
+      uint64_t* empty = is_v ? (NQ ? o_done : v_empty) : (NQ ? s_full : k_empty);
       int qc = 0, slot = 0;              // Q tiles loaded; this warp's next slot
       unsigned int turn = 0;             // parity of the turn around the ring
       bool round = false;                // the ring has been around once
@@ -662,12 +677,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (lane < nbox && lane * p.box_rows < e && (lane + 1) * p.box_rows > a) {
           const int at = p.block_size <= 128 ? j * nbox + lane : j * 128 / p.block_size;
           pg = p.block_table[static_cast<size_t>(it.key0) * p.max_blocks + at];
-          if (pg < 0 || pg >= p.num_blocks) {
-            atomicCAS(p.status, 0u, kStatusInvalid | (kPSiteBlock << 8));
-            pg = p.num_blocks;  // outside the map: reads as zeros
-          }
         }
-        return pg;
+        return pg;  // not looked at here: the load goes on behind the tile before
       };
       auto load_tile = [&](const SeqItem& it, int j, int pg, uint8_t* dst, uint64_t* bar) {
         if constexpr (!PAGED) {
@@ -682,6 +693,10 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const int i0 = a / p.box_rows, n = (e + p.box_rows - 1) / p.box_rows - i0;
           const int row = p.block_size <= 128 ? 0 : j * 128 % p.block_size;
           if (lane == 0) mbar_arrive_expect_tx(bar, n * p.box_rows * 128 * C::KCH);
+          if (pg < 0 || pg >= p.num_blocks) {
+            atomicCAS(p.status, 0u, kStatusInvalid | (kPSiteBlock << 8));
+            pg = p.num_blocks;  // outside the map: reads as zeros
+          }
           __syncwarp();
 #pragma unroll 1
           for (int i = i0; i < i0 + n; ++i) {
@@ -769,89 +784,102 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
       }
       __syncwarp();
-    } else if (NQ > 0 && lane == 0) {
+    } else if constexpr (NQ > 0) {
       // ---------------------------------------------------------------- MMA issuer, few rows
       // S^T = K Q^T (128 keys x NQ rows) runs kLag steps ahead of O^T += V^T P^T (head columns
       // x NQ rows); step c is warpgroup c & 1's, with an accumulator of its own.
+      // One thread feeds both products; what it does a step bounds the loop on 64-column heads,
+      // so a step has two commits and three waits: S block and K slot c % KS share s_full, V slot
+      // e % VS has o_done (VS even: always the same warpgroup's), and an S block is free by the
+      // time its turn comes again, since the P made from it has been waited for (kLag < KS).
       constexpr int N = NQ ? NQ : 16;  // (NQ = 0: not reached)
       constexpr int kLag = 2;
+      static_assert(NQ == 0 || (kLag < C::KS && C::VS % 2 == 0), "few-rows rings");
       constexpr uint32_t id_s = idesc_f16(128, N, BF16, false, false);
       constexpr uint32_t id_o = idesc_f16(128, N, BF16, true, false);
       const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dV = sdesc_sw128(smem_u32(sV), C::CHUNK, 1024), dP = sdesc_sw128(smem_u32(sP), 16, 1024);
       int ii = 0, qc = 0;
-      int c = 0;                 // steps whose S has been issued
-      int left = 0;              // steps of the current item still to issue
-      int begun = 0;             // steps of the current item issued
-      int oc0 = 0, oc1 = 0;      // items begun per accumulator
-      unsigned int first = 0;    // bit 0: the newest step was the first of its accumulator in its item
+      int c = 0, e = 0;             // steps whose S has been issued, and whose P V has
+      int ks = 0, vs = 0;           // their slots
+      uint32_t kpar = 0, vpar = 0;  // parity of the turns around the rings
+      int left = 0, begun = 0;      // steps of the current item still to issue, and issued
+      int oc0 = 0, oc1 = 0;         // items begun per accumulator
+      unsigned int first = 0;       // bit c & 7: step c was the first of its accumulator in its item
+      uint64_t q = dQ;
+      const bool leader = elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, site)) != 0;
+      };
       bool ok = true, more = true;
-      for (int i = 0; ok; ++i) {
-        if (left == 0 && more) {
-          for (;; ++ii) {  // the next item with key tiles
-            ok = mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem);
-            if (!ok) break;
-            more = items[ii % NI].valid != 0;
-            left = more ? items[ii % NI].n : 0;
-            mbar_arrive(&item_empty[ii % NI]);
-            if (!more || left > 0) break;
-          }
-          if (!ok) break;
+      for (;;) {
+        // The next item.  With products outstanding it is taken only if it is there: it may be
+        // waiting for a ring slot that is freed behind one of them.
+        if (left == 0 && more && (c == e || __all_sync(0xffffffffu, mbar_test(&item_full[ii % NI], (ii / NI) & 1)))) {
+          if (!(ok = wait(&item_full[ii % NI], (ii / NI) & 1, kQSiteItem))) break;
+          left = __shfl_sync(0xffffffffu, items[ii % NI].valid ? items[ii % NI].n : -1, 0);
+          more = left >= 0;
+          left = max(left, 0);
+          if (leader) mbar_arrive(&item_empty[ii % NI]);
           ++ii;
           begun = 0;
-          if (more) ok = mbar_wait(&q_full[qc % C::QS], (qc / C::QS) & 1, wc, kQSiteMmaQ);
-          if (!ok) break;
+          if (left > 0) {
+            if (!(ok = wait(&q_full[qc & 1], (qc >> 1) & 1, kQSiteMmaQ))) break;
+            q = sdesc_add(dQ, (qc & 1) * C::QTILE);
+          } else if (more) {
+            continue;
+          }
         }
-        first <<= 1;
         if (left > 0) {
-          const int b = c & 3, ks = c % C::KS;
-          ok = mbar_wait(&k_full[ks], (c / C::KS) & 1, wc, kQSiteMmaK);
-          if (ok && c >= 4) ok = mbar_wait(&s_free[b], ((c >> 2) - 1) & 1, wc, kQSiteMmaP);
-          if (!ok) break;
+          if (!(ok = wait(&k_full[ks], kpar, kQSiteMmaK))) break;
           tc_fence_after();
-          const uint64_t da = sdesc_add(dK, ks * C::TILE), db = sdesc_add(dQ, (qc % C::QS) * C::QTILE);
+          const uint64_t da = sdesc_add(dK, ks * C::TILE);
+          if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tbase + b * N, sdesc_add(da, (kk >> 2) * C::CHUNK + (kk & 3) * 32),
-                    sdesc_add(db, (kk >> 2) * C::QCHUNK + (kk & 3) * 32), id_s, kk > 0);
-          umma_commit(&s_full[b]);
-          umma_commit(&k_empty[ks]);
-          if (--left == 0) {
-            umma_commit(&q_empty[qc % C::QS]);
-            ++qc;
+            umma_ss(tbase + ks * N, sdesc_add(da, (kk >> 2) * C::CHUNK + (kk & 3) * 32),
+                    sdesc_add(q, (kk >> 2) * C::QCHUNK + (kk & 3) * 32), id_s, kk > 0);
+          umma_commit(&s_full[ks]);
+          if (left == 1) umma_commit(&q_empty[qc & 1]);
           }
-          first |= begun < 2 ? 1u : 0u;
+          if (--left == 0) ++qc;
+          if (++ks == C::KS) ks = 0, kpar ^= 1;
+          first = begun < 2 ? first | (1u << (c & 7)) : first & ~(1u << (c & 7));
           ++begun;
           ++c;
-        } else if (i >= c + kLag) {
-          break;  // nothing left to issue and every P V is out
+          if (c - e <= kLag) continue;
+        } else if (c == e) {
+          if (!more) break;
+          continue;
         }
-        const int e = i - kLag;  // step of this round's P V
-        if (e < 0 || e >= c) continue;
-        const int w = e & 1, vs = e % C::VS;
-        const bool new_item = first >> kLag & 1;
-        ok = mbar_wait(&v_full[vs], (e / C::VS) & 1, wc, kQSiteMmaV) &&
-             mbar_wait(&p_ready[w], (e >> 1) & 1, wc, kQSiteMmaP);
+        const int w = e & 1, pb = w * 2 + (e >> 1) % C::PB;
+        const bool new_item = first >> (e & 7) & 1;
+        ok = wait(&v_full[vs], vpar, kQSiteMmaV) &&
+             wait(&p_ready[pb], ((e >> 1) / C::PB) & 1, kQSiteMmaP);
         if (ok && new_item) {
           int& oc = w ? oc1 : oc0;
-          if (oc > 0) ok = mbar_wait(&o_free[w], (oc - 1) & 1, wc, kQSiteMmaO);
+          if (oc > 0) ok = wait(&o_free[w], (oc - 1) & 1, kQSiteMmaO);
           ++oc;
         }
         if (!ok) break;
         tc_fence_after();
-        const uint64_t da = sdesc_add(dV, vs * C::TILE), db = sdesc_add(dP, w * C::PBUF);
+        const uint64_t da = sdesc_add(dV, vs * C::TILE);
+        const uint64_t db = sdesc_add(dP, (w * C::PB + (e >> 1) % C::PB) * C::PBUF);
+        if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           umma_ss(tbase + C::O_COL(w), sdesc_add(da, kk * 2048),
                   sdesc_add(db, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_o, (kk > 0 || !new_item) ? 1u : 0u);
-        umma_commit(&o_done[w]);
-        umma_commit(&v_empty[vs]);
+        umma_commit(&o_done[vs]);
+        }
+        ++e;
+        if (++vs == C::VS) vs = 0, vpar ^= 1;
       }
-      umma_commit(&drain);
+      if (leader) umma_commit(&drain);
       volatile int no_abort = 0;
       WaitCtl dw{p.status, &no_abort, p.wait_ns};
       mbar_wait(&drain, 0, dw, kQSiteMmaDrain);
-    } else if (NQ == 0 && lane == 0) {
+    } else if (lane == 0) {
       // ---------------------------------------------------------------- MMA issuer (warp 9)
       // One loop over the key tiles of all items.  Step j issues P V of its own tile and S of
       // the step after it, which may be the next item's first; the loop begins with a step
@@ -1009,8 +1037,13 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t wg_bar = 1 + w;
     const int G = p.G;
     const float sl2 = p.scale_log2;
-    uint8_t* myP = sP + w * C::PBUF;
+    uint8_t* myP = sP + w * C::PB * C::PBUF;
     int c = 0, pc = 0;  // steps before this item; steps of this warpgroup
+    // Product k of this warpgroup.  (Its barrier's next phase is this warpgroup's too, VS being
+    // even, and needs a P that is not written yet: no wait is more than one phase behind.)
+    auto product = [&](int k) {  // step 2 k + w of all
+      return mbar_wait(&o_done[(2 * k + w) % C::VS], ((2 * k + w) / C::VS) & 1, wc, kQSiteSoftO);
+    };
     for (int ii = 0;; ++ii) {
       // Waits end in a vote of all that share a named barrier, which has no time limit.
       if (!named_bar_and(3, 256, mbar_wait(&item_full[ii % NI], (ii / NI) & 1, wc, kQSiteItem))) break;
@@ -1027,21 +1060,19 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       bool ok = true;
       const int s0 = (c & 1) == w ? 0 : 1;
       for (int s = s0; s < steps; s += 2) {
-        const int b = (c + s) & 3;
-        // This step's scores, and P's buffer free of the product before.
-        bool got = mbar_wait(&s_full[b], ((c + s) >> 2) & 1, wc, kQSiteSoftS);
-        if (got && pc > 0) got = mbar_wait(&o_done[w], (pc - 1) & 1, wc, kQSiteSoftO);
-        ok = named_bar_and(wg_bar, 128, got);
-        if (!ok) break;
-        tc_fence_after();
+        const int b = (c + s) % C::KS;
+        // This step's scores, and P's buffer free of the product that read it last.
+        bool got = mbar_wait(&s_full[b], ((c + s) / C::KS) & 1, wc, kQSiteSoftS);
+        if (got && pc >= C::PB) got = product(pc - C::PB);
+        got = __all_sync(0xffffffffu, got);
         uint32_t sr[N];
-        if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, b * N), sr);
-        else tmem_ld32(tmem_addr(tbase, lb, b * N), sr);
-        tmem_wait_ld();
-        reg_fence(sr);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[b]);
+        if (got) {
+          tc_fence_after();
+          if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, b * N), sr);
+          else tmem_ld32(tmem_addr(tbase, lb, b * N), sr);
+          tmem_wait_ld();
+          reg_fence(sr);
+        }
         const int kc0 = (j0 + s) * 128, key = kc0 + r;
         const bool masked = kc0 + 127 > sure_hi || kc0 < sure_lo;
         float x[N];
@@ -1064,8 +1095,15 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (n < rows) wm[n] = warp_max(x[n]);
           need |= wm[n] - m[n] > 8.0f;
         }
-        if (!named_bar_and(wg_bar, 128, !need)) {
-          float* ex = reinterpret_cast<float*>(myP);  // [4][N]
+        // One vote a step: no exchange, and nobody's wait ran out.
+        if (!named_bar_and(wg_bar, 128, got && !need)) {
+          // The accumulator's last product is done before it is rescaled (and P's other buffer,
+          // which takes the maxima, free).
+          if (got && pc > 0) got = product(pc - 1);
+          ok = named_bar_and(wg_bar, 128, got);
+          if (!ok) break;
+          tc_fence_after();
+          float* ex = reinterpret_cast<float*>(myP + pc % C::PB * C::PBUF);  // [4][N]
           if (lane < N) {
             float mine = wm[0];
 #pragma unroll
@@ -1083,7 +1121,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             l[n] *= f[n];
             lr[n] *= f[n];
           }
-          if (s != s0) {  // the accumulator (its last product has been waited for)
+          if (s != s0) {
             uint32_t o[N];
             if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, C::O_COL(w)), o);
             else tmem_ld32(tmem_addr(tbase, lb, C::O_COL(w)), o);
@@ -1099,10 +1137,11 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           named_bar_sync(wg_bar, 128);  // every warp has read the maxima: P may go over them
         }
         // P^T, K-major rows of 64 keys with 128-byte swizzle: 16-byte unit u of row n at u ^ (n % 8).
-        uint8_t* dst = myP + (r >> 6) * (N * 128) + (r & 7) * 2;
+        uint8_t* dst = myP + pc % C::PB * C::PBUF + (r >> 6) * (N * 128) + (r & 7) * 2;
         const int u = (r & 63) >> 3;
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
+          if (n >= rows) continue;  // columns of no row: nothing reads their output
           const float e0 = ex2_approx(x[n] - (m[n] == -INFINITY ? 0.f : m[n]));
           const float e1 = ex2_approx(x[n + 1] - (m[n + 1] == -INFINITY ? 0.f : m[n + 1]));
           const uint32_t pk = pack2<BF16>(e0, e1);
@@ -1118,13 +1157,13 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[w]);
+        if (lane == 0) mbar_arrive(&p_ready[w * 2 + pc % C::PB]);
         ++pc;
       }
       // The item's end: the sums over the keys, then both warpgroups' parts joined.
       const bool mine = steps > s0;  // this warpgroup had steps
-      if (ok && mine) ok = mbar_wait(&o_done[w], (pc - 1) & 1, wc, kQSiteSoftO);
-      float* ex = reinterpret_cast<float*>(myP);  // [4][2][N] sums, [N] maxima
+      if (ok && mine) ok = product(pc - 1);
+      float* ex = reinterpret_cast<float*>(myP);  // [4][2][N] sums, [N] maxima (P is not read any more)
       if (steps > 0) {
         // Lane n < N ends up with the warp's sums of row n.
         float sl = 0.f, sr2 = 0.f, mm = -INFINITY;
@@ -1153,7 +1192,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       tc_fence_after();
       constexpr int H2 = N / 2;  // rows of this warpgroup's half
       const float* e0 = reinterpret_cast<const float*>(sP);
-      const float* e1 = reinterpret_cast<const float*>(sP + C::PBUF);
+      const float* e1 = reinterpret_cast<const float*>(sP + C::PB * C::PBUF);
       const int n0 = w * H2;
       if (n0 < rows) {
         uint32_t o0[H2], o1[H2];

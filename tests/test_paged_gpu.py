@@ -148,6 +148,20 @@ def test_more_queries_than_keys():
         assert not o.any() and (lse == float("-inf")).all()
 
 
+@pytest.mark.parametrize("n", [1, 9, 40, 700])
+@pytest.mark.parametrize("d", [64, 256])
+def test_requests_without_keys_between_others(n, d):
+    """Many blocks of rows that see no key, between requests that have keys."""
+    s = Step([100, 0, 0, 0, 0, 200, 0], [1, n, n, n, n, 2, n], 4, 2, d, 16, "bf16", seed=n)
+    s.lens = ints([101, 0, 0, 0, 0, 202, 0])
+    caches = [(k[:m], v[:m]) for (k, v), m in zip(s.caches, (101, 0, 0, 0, 0, 202, 0))]
+    for causal in (True, False):
+        o, lse = s.run(causal)
+        ro, rl, bo, bl = packed_forward(s.q, None, None, s.new, s.scale, causal, 0, caches)
+        assert_within(o, ro, bo, "O")
+        assert_within(lse, rl, bl, "LSE")
+
+
 def test_rows_behind_the_last_sequence_and_the_workspace_end():
     s = Step([100, 300], [1, 20], 8, 2, 128, 16, "bf16", seed=9)
     T = 21

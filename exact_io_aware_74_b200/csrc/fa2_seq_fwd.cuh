@@ -71,14 +71,17 @@ struct SeqCfg {
   // Ring stages within 227 KB (tiles of 16, 32, 48, 64 KB).  Two query tiles have a third
   // slot at D = 128, so that the next item's first tile loads during this one.
   static constexpr int QS = NQ ? 2 : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 3 : 2) : 1));
-  // (Few rows: as many S blocks as K slots; V slots in even number, see the issuer.)
-  static constexpr int KS = NQ ? (D == 64 ? 6 : 4) : (D == 64 ? 4 : (D == 256 ? 1 : 2));
-  static constexpr int VS = NQ ? (D == 64 ? 6 : 2) : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1));
+  // (Few rows: as many S blocks as K slots; with V slots in even number a product's barrier
+  // releases its slot too, see the issuer.  Three slots each at D = 128: 4 and 2 took 275, not
+  // 264 us for 64 requests over 6k tokens in blocks of 64, B200.)
+  static constexpr int KS = NQ ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : (D == 256 ? 1 : 2));
+  static constexpr int VS = NQ ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : (D == 128 ? (QT == 2 ? 2 : 3) : 1));
   // Few rows: P^T of each warpgroup, two chunks of 64 keys, PB buffers each (with two a
   // warpgroup need not wait for its last product before it writes the next P).  (At D = 64 the V operand's
   // upper 64 rows are whatever lies 16 KB behind the tile: at least that much follows.)
   static constexpr int PBUF = 2 * NQ * 128, PB = NQ == 16 && D == 64 ? 2 : 1;
-  static_assert(NQ == 0 || (VS % 2 == 0 && 2 * PB <= VS), "a product's barrier comes round after its P buffer");
+  static constexpr bool SHARE_V = NQ && VS % 2 == 0;
+  static_assert(NQ == 0 || PB == 1 || (SHARE_V && 2 * PB <= VS), "a product's barrier comes round after its P buffer");
   static constexpr int PREST = QS * QTILE + 2 * PB * PBUF;
   static constexpr int REST = NQ ? (PREST < CHUNK ? CHUNK : PREST) : QS * TILE;
   static constexpr int SMEM = (KS + VS) * TILE + REST + 1024;
@@ -659,7 +662,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int slots = is_v ? C::VS : C::KS;
       uint64_t* full = is_v ? v_full : k_full;
       // Few rows: a product's completion barrier is its slot's release too.
-      uint64_t* empty = is_v ? (NQ ? o_done : v_empty) : (NQ ? s_full : k_empty);
+      uint64_t* empty = is_v ? (C::SHARE_V ? o_done : v_empty) : (NQ ? s_full : k_empty);
       int qc = 0, slot = 0;              // Q tiles loaded; this warp's next slot
       unsigned int turn = 0;             // parity of the turn around the ring
       bool round = false;                // the ring has been around once
@@ -789,12 +792,13 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // S^T = K Q^T (128 keys x NQ rows) runs kLag steps ahead of O^T += V^T P^T (head columns
       // x NQ rows); step c is warpgroup c & 1's, with an accumulator of its own.
       // One thread feeds both products; what it does a step bounds the loop on 64-column heads,
-      // so a step has two commits and three waits: S block and K slot c % KS share s_full, V slot
-      // e % VS has o_done (VS even: always the same warpgroup's), and an S block is free by the
-      // time its turn comes again, since the P made from it has been waited for (kLag < KS).
+      // so a step has few commits and three waits: S block and K slot c % KS share s_full, V slot
+      // e % VS has o_done where VS is even (a slot's products are then always the same
+      // warpgroup's), and an S block is free by the time its turn comes again, since the P made
+      // from it has been waited for (kLag < KS).
       constexpr int N = NQ ? NQ : 16;  // (NQ = 0: not reached)
       constexpr int kLag = 2;
-      static_assert(NQ == 0 || (kLag < C::KS && C::VS % 2 == 0), "few-rows rings");
+      static_assert(NQ == 0 || kLag < C::KS, "few-rows rings");
       constexpr uint32_t id_s = idesc_f16(128, N, BF16, false, false);
       constexpr uint32_t id_o = idesc_f16(128, N, BF16, true, false);
       const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
@@ -870,7 +874,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (int kk = 0; kk < 8; ++kk)
           umma_ss(tbase + C::O_COL(w), sdesc_add(da, kk * 2048),
                   sdesc_add(db, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_o, (kk > 0 || !new_item) ? 1u : 0u);
-        umma_commit(&o_done[vs]);
+        umma_commit(&o_done[C::SHARE_V ? vs : w]);
+        if (!C::SHARE_V) umma_commit(&v_empty[vs]);
         }
         ++e;
         if (++vs == C::VS) vs = 0, vpar ^= 1;
@@ -1042,6 +1047,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // Product k of this warpgroup.  (Its barrier's next phase is this warpgroup's too, VS being
     // even, and needs a P that is not written yet: no wait is more than one phase behind.)
     auto product = [&](int k) {  // step 2 k + w of all
+      if (!C::SHARE_V) return mbar_wait(&o_done[w], k & 1, wc, kQSiteSoftO);
       return mbar_wait(&o_done[(2 * k + w) % C::VS], ((2 * k + w) / C::VS) & 1, wc, kQSiteSoftO);
     };
     for (int ii = 0;; ++ii) {

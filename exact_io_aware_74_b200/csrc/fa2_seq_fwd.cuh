@@ -23,8 +23,8 @@
 // Roles (384 threads, three warpgroups):
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1 (QT = 1: warps 4-7 idle)
 //   warp 8          Q and K tiles by TMA; pages one box each
-//   warp 9          MMA issuer (one thread)
-//   warp 10         scheduler: finds the CTA's next item while the current one runs
+//   warp 9          MMA issuer (one thread; few rows: scheduler and issuer of S)
+//   warp 10         (few rows: issuer of P V) scheduler: finds the CTA's next item while the current one runs
 //   warp 11         V tiles by TMA; zeroes the rows that belong to no visible key (a sequence
 //                   that ends inside a tile), so that nothing there, NaN included, reaches P V
 // The CTA runs its items as one stream: the rings of Q, K and V tiles and every barrier's
@@ -310,6 +310,67 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
   return true;
 }
 
+// The items of one CTA's share, one after the other.  Whole warp.
+template <int QT>
+struct ShareWalk {
+  long long per, x, xe;  // units to a share; next unit, end
+  UnitAt u;
+
+  __device__ __forceinline__ void start(const SeqParams& p, int* held, int lane) {
+    const int c = blockIdx.x;
+    if (lane == 0) p.merge[c] = make_int4(0, 0, 0, 0);  // nothing to merge, until a block is cut
+    if (!find_share<QT>(p, gridDim.x, c, held, lane, per, x, xe, u)) x = xe = 0;
+  }
+  // The next item with key tiles; false at the end of the share.
+  __device__ __forceinline__ bool next(const SeqParams& p, int lane, SeqItem& it) {
+    const int c = blockIdx.x, R = QT * p.tpt;
+    bool found = false;
+#pragma unroll 1
+    while (!found && x < xe) {
+      const int len = block_units<QT>(p, u.s.n, u.s.nk, u.blk);
+      const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
+      make_item<true, QT>(p, u.s, u.b, u.kvh, u.blk, it);
+      // Key tiles [a, e) of the block's fall into this share.
+      constexpr int C0 = kItemUnits<QT>;
+      const int a = max(0, u.at - C0), e = max(0, u.at + take - C0);
+      if (it.n == 0) {
+        // Rows that see no key: O = 0 and LSE = -inf, here.  (The other roles then never meet
+        // an item without key tiles, which would be in the way of the next one.)
+        if (e > a)
+          for (int r = 0; r < it.n_tok * p.G; ++r) {
+            const int row = it.row0 + r / p.G, head = u.kvh * p.G + r % p.G;
+            if (lane * 8 < p.d)
+              *reinterpret_cast<uint4*>(p.O + row * p.o_row + head * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
+            if (lane == 0) p.LSE[static_cast<size_t>(head) * p.T + row] = -INFINITY;
+          }
+      } else if (e > a) {
+        found = true;
+        if (a > 0 || e < len - C0) {
+          if (a == 0 && lane == 0) {
+            // The block goes on in the next shares: for the merge kernel.
+            int parts = 1;
+            for (long long end = xe; end < x + len - u.at; end += per) ++parts;
+            p.merge[c] = make_int4(it.row0, it.n_tok, u.kvh, parts);
+          }
+          cut_item(it, a, e);
+          it.part = 2 * c + (a > 0 ? 0 : 1);
+        }
+      }
+      x += take;
+      if (x >= xe) break;
+      u.at = 0;
+      if (++u.blk * R >= u.s.n) {
+        u.blk = 0;
+        if (++u.kvh >= p.Hkv) {
+          u.kvh = 0;
+          do u.s = seq_len<true>(p, ++u.b); while (u.s.n == 0 && u.b + 1 < p.B);  // units are left
+        }
+      }
+    }
+    return found;
+  }
+};
+
 __device__ __forceinline__ int rows_of(const int* cu, int T, int b) {
   const int s = min(max(cu[b], 0), T);
   return min(max(cu[b + 1], s), T) - s;
@@ -499,7 +560,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __shared__ uint64_t item_full[NI], item_empty[NI], clc_full;
   __shared__ uint64_t q_full[C::QS], q_empty[C::QS], k_full[C::KS], k_empty[C::KS];
   __shared__ uint64_t v_full[C::VS], v_empty[C::VS], v_raw[C::VS];
-  __shared__ uint64_t s_full[6], s_free[2], p_ready[4], o_done[6], o_free[2], drain;
+  __shared__ uint64_t s_full[6], s_free[6], p_ready[4], o_done[6], o_free[2], drain, drain_pv;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int held[kHeld];  // the scheduling warp's
@@ -514,15 +575,15 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     abort_flag = 0;
     for (int i = 0; i < NI; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 3 + (NQ ? 8 : 4 * QT));  // two producers, MMA and the softmax warps
+      mbar_init(&item_empty[i], NQ ? 12 : 3 + 4 * QT);  // two producers, the issuers and the softmax warps
     }
     for (int i = 0; i < 6; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&p_ready[i], 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_free[i], 4);
       mbar_init(&o_free[i], NQ ? 8 : 4);
     }
     mbar_init(&clc_full, 1);
@@ -534,6 +595,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       mbar_init(&v_raw[i], 1);
     }
     mbar_init(&drain, 1);
+    mbar_init(&drain_pv, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -550,7 +612,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   if (warp >= 8) {
     regs_dec<C::OTHER_REGS>();
-    if (warp == 10) {
+    if (NQ == 0 && warp == 10) {
       // ---------------------------------------------------------------- scheduler
       int ii = 0;
       auto publish = [&](const SeqItem& it) -> bool {
@@ -568,55 +630,9 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       SeqItem it{};
       bool ok = true;
       if constexpr (PAGED) {
-        const int c = blockIdx.x;
-        if (lane == 0) p.merge[c] = make_int4(0, 0, 0, 0);  // nothing to merge, until a block is cut
-        long long per, x, xe;
-        UnitAt u;
-        if (find_share<QT>(p, gridDim.x, c, held, lane, per, x, xe, u)) {
-          const int R = QT * p.tpt;
-#pragma unroll 1
-          while (ok) {
-            const int len = block_units<QT>(p, u.s.n, u.s.nk, u.blk);
-            const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
-            make_item<true, QT>(p, u.s, u.b, u.kvh, u.blk, it);
-            // Key tiles [a, e) of the block's fall into this share.
-            constexpr int C0 = kItemUnits<QT>;
-            const int a = max(0, u.at - C0), e = max(0, u.at + take - C0);
-            if (it.n == 0) {
-              // Rows that see no key: O = 0 and LSE = -inf, here.  (The other roles then never
-              // meet an item without key tiles, which would be in the way of the next one.)
-              if (e > a)
-                for (int r = 0; r < it.n_tok * p.G; ++r) {
-                  const int row = it.row0 + r / p.G, head = u.kvh * p.G + r % p.G;
-                  if (lane * 8 < p.d)
-                    *reinterpret_cast<uint4*>(p.O + row * p.o_row + head * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
-                  if (lane == 0) p.LSE[static_cast<size_t>(head) * p.T + row] = -INFINITY;
-                }
-            } else if (e > a) {
-              if (a > 0 || e < len - C0) {
-                if (a == 0 && lane == 0) {
-                  // The block goes on in the next shares: for the merge kernel.
-                  int parts = 1;
-                  for (long long end = xe; end < x + len - u.at; end += per) ++parts;
-                  p.merge[c] = make_int4(it.row0, it.n_tok, u.kvh, parts);
-                }
-                cut_item(it, a, e);
-                it.part = 2 * c + (a > 0 ? 0 : 1);
-              }
-              ok = publish(it);
-            }
-            x += take;
-            if (x >= xe) break;
-            u.at = 0;
-            if (++u.blk * R >= u.s.n) {
-              u.blk = 0;
-              if (++u.kvh >= p.Hkv) {
-                u.kvh = 0;
-                do u.s = seq_len<true>(p, ++u.b); while (u.s.n == 0 && u.b + 1 < p.B);  // units are left
-              }
-            }
-          }
-        }
+        ShareWalk<QT> walk;
+        walk.start(p, held, lane);
+        while (ok && walk.next(p, lane, it)) ok = publish(it);
       } else {
         const int R = QT * p.tpt;
         BlockOrder<kHeld> order;
@@ -788,102 +804,116 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       __syncwarp();
     } else if constexpr (NQ > 0) {
-      // ---------------------------------------------------------------- MMA issuer, few rows
-      // S^T = K Q^T (128 keys x NQ rows) runs kLag steps ahead of O^T += V^T P^T (head columns
-      // x NQ rows); step c is warpgroup c & 1's, with an accumulator of its own.
-      // One thread feeds both products; what it does a step bounds the loop on 64-column heads,
-      // so a step has few commits and three waits: S block and K slot c % KS share s_full, V slot
-      // e % VS has o_done where VS is even (a slot's products are then always the same
-      // warpgroup's), and an S block is free by the time its turn comes again, since the P made
-      // from it has been waited for (kLag < KS).
-      constexpr int N = NQ ? NQ : 16;  // (NQ = 0: not reached)
-      constexpr int kLag = 2;
-      static_assert(NQ == 0 || kLag < C::KS, "few-rows rings");
-      constexpr uint32_t id_s = idesc_f16(128, N, BF16, false, false);
-      constexpr uint32_t id_o = idesc_f16(128, N, BF16, true, false);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_u32(sV), C::CHUNK, 1024), dP = sdesc_sw128(smem_u32(sP), 16, 1024);
-      int ii = 0, qc = 0;
-      int c = 0, e = 0;             // steps whose S has been issued, and whose P V has
-      int ks = 0, vs = 0;           // their slots
-      uint32_t kpar = 0, vpar = 0;  // parity of the turns around the rings
-      int left = 0, begun = 0;      // steps of the current item still to issue, and issued
-      int oc0 = 0, oc1 = 0;         // items begun per accumulator
-      unsigned int first = 0;       // bit c & 7: step c was the first of its accumulator in its item
-      uint64_t q = dQ;
-      const bool leader = elect_one();
+      // ---------------------------------------------------------------- issuers, few rows
+      // S^T = K Q^T (128 keys x NQ rows) and O^T += V^T P^T (head columns x NQ rows); step c is
+      // warpgroup c & 1's, with an accumulator of its own.  The issuing itself bounds a step on
+      // 64-column heads (some 1700 cycles for both products from one thread, of which the tensor
+      // pipe works 780), so the products have a warp each: warp 9 issues S, and finds the
+      // items, which it has to know first; warp 10 issues P V.  S block and K slot c % KS share
+      // s_full, V slot e % VS has o_done where VS is even (a slot's products are then always the
+      // same warpgroup's).
+      constexpr uint32_t id_s = idesc_f16(128, NQ, BF16, false, false);
+      constexpr uint32_t id_o = idesc_f16(128, NQ, BF16, true, false);
+      const bool leader = elect_one();  // the warp waits together, one thread issues
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, site)) != 0;
       };
-      bool ok = true, more = true;
-      for (;;) {
-        // The next item.  With products outstanding it is taken only if it is there: it may be
-        // waiting for a ring slot that is freed behind one of them.
-        if (left == 0 && more && (c == e || __all_sync(0xffffffffu, mbar_test(&item_full[ii % NI], (ii / NI) & 1)))) {
+      bool ok = true;
+      int slot = 0;
+      uint32_t par = 0;  // parity of the turn around the ring
+      if (warp == 9) {
+        const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+        ShareWalk<QT> walk;
+        walk.start(p, held, lane);
+        SeqItem it{};
+        bool have = walk.next(p, lane, it);  // `it` is still to be handed out
+        int out = 0, in = 0, c = 0;          // items handed out, and begun here; steps issued
+        bool ended = false;
+        for (;;) {
+          // Items go out as ring slots come free; waited for only when there is none to begin.
+          while (ok && !ended) {
+            const int s = out % NI;
+            if (out >= NI) {
+              const uint32_t turn = ((out / NI) - 1) & 1;
+              if (out > in && !__all_sync(0xffffffffu, mbar_test(&item_empty[s], turn))) break;
+              if (!(ok = wait(&item_empty[s], turn, kQSiteItemEmpty))) break;
+            }
+            if (!have) it.valid = 0, ended = true;
+            if (leader) {
+              items[s] = it;
+              mbar_arrive(&item_full[s]);
+            }
+            __syncwarp();
+            ++out;
+            if (have) have = walk.next(p, lane, it);
+          }
+          if (!ok) break;
+          // The next item is begun.  (Its slot was written by this warp.)
+          const int s = in % NI;
+          const int n = __shfl_sync(0xffffffffu, items[s].valid ? items[s].n : 0, 0);
+          __syncwarp();
+          if (leader) mbar_arrive(&item_empty[s]);
+          if (n == 0) break;  // the end
+          if (!(ok = wait(&q_full[in & 1], (in >> 1) & 1, kQSiteMmaQ))) break;
+          const uint64_t q = sdesc_add(dQ, (in & 1) * C::QTILE);
+          for (int i = 0; i < n; ++i, ++c) {
+            ok = wait(&k_full[slot], par, kQSiteMmaK) && (c < C::KS || wait(&s_free[slot], par ^ 1, kQSiteMmaP));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t da = sdesc_add(dK, slot * C::TILE);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_ss(tbase + slot * NQ, sdesc_add(da, (kk >> 2) * C::CHUNK + (kk & 3) * 32),
+                        sdesc_add(q, (kk >> 2) * C::QCHUNK + (kk & 3) * 32), id_s, kk > 0);
+              umma_commit(&s_full[slot]);
+              if (i + 1 == n) umma_commit(&q_empty[in & 1]);
+            }
+            if (++slot == C::KS) slot = 0, par ^= 1;
+          }
+          if (!ok) break;
+          ++in;
+        }
+      } else {
+        const uint64_t dV = sdesc_sw128(smem_u32(sV), C::CHUNK, 1024), dP = sdesc_sw128(smem_u32(sP), 16, 1024);
+        int e = 0, oc0 = 0, oc1 = 0;  // steps issued; items begun per accumulator
+        for (int ii = 0; ok; ++ii) {
           if (!(ok = wait(&item_full[ii % NI], (ii / NI) & 1, kQSiteItem))) break;
-          left = __shfl_sync(0xffffffffu, items[ii % NI].valid ? items[ii % NI].n : -1, 0);
-          more = left >= 0;
-          left = max(left, 0);
+          const int n = __shfl_sync(0xffffffffu, items[ii % NI].valid ? items[ii % NI].n : 0, 0);
+          __syncwarp();
           if (leader) mbar_arrive(&item_empty[ii % NI]);
-          ++ii;
-          begun = 0;
-          if (left > 0) {
-            if (!(ok = wait(&q_full[qc & 1], (qc >> 1) & 1, kQSiteMmaQ))) break;
-            q = sdesc_add(dQ, (qc & 1) * C::QTILE);
-          } else if (more) {
-            continue;
+          if (n == 0) break;
+          for (int i = 0; i < n; ++i, ++e) {
+            const int w = e & 1, pb = w * 2 + (e >> 1) % C::PB;
+            ok = wait(&v_full[slot], par, kQSiteMmaV) && wait(&p_ready[pb], ((e >> 1) / C::PB) & 1, kQSiteMmaP);
+            if (ok && i < 2) {
+              // The first product of an accumulator overwrites it: read out by then.
+              int& oc = w ? oc1 : oc0;
+              if (oc > 0) ok = wait(&o_free[w], (oc - 1) & 1, kQSiteMmaO);
+              ++oc;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t da = sdesc_add(dV, slot * C::TILE);
+              const uint64_t db = sdesc_add(dP, (w * C::PB + (e >> 1) % C::PB) * C::PBUF);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_ss(tbase + C::O_COL(w), sdesc_add(da, kk * 2048),
+                        sdesc_add(db, (kk >> 2) * (NQ * 128) + (kk & 3) * 32), id_o, (kk > 0 || i >= 2) ? 1u : 0u);
+              umma_commit(&o_done[C::SHARE_V ? slot : w]);
+              if (!C::SHARE_V) umma_commit(&v_empty[slot]);
+            }
+            if (++slot == C::VS) slot = 0, par ^= 1;
           }
         }
-        if (left > 0) {
-          if (!(ok = wait(&k_full[ks], kpar, kQSiteMmaK))) break;
-          tc_fence_after();
-          const uint64_t da = sdesc_add(dK, ks * C::TILE);
-          if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tbase + ks * N, sdesc_add(da, (kk >> 2) * C::CHUNK + (kk & 3) * 32),
-                    sdesc_add(q, (kk >> 2) * C::QCHUNK + (kk & 3) * 32), id_s, kk > 0);
-          umma_commit(&s_full[ks]);
-          if (left == 1) umma_commit(&q_empty[qc & 1]);
-          }
-          if (--left == 0) ++qc;
-          if (++ks == C::KS) ks = 0, kpar ^= 1;
-          first = begun < 2 ? first | (1u << (c & 7)) : first & ~(1u << (c & 7));
-          ++begun;
-          ++c;
-          if (c - e <= kLag) continue;
-        } else if (c == e) {
-          if (!more) break;
-          continue;
-        }
-        const int w = e & 1, pb = w * 2 + (e >> 1) % C::PB;
-        const bool new_item = first >> (e & 7) & 1;
-        ok = wait(&v_full[vs], vpar, kQSiteMmaV) &&
-             wait(&p_ready[pb], ((e >> 1) / C::PB) & 1, kQSiteMmaP);
-        if (ok && new_item) {
-          int& oc = w ? oc1 : oc0;
-          if (oc > 0) ok = wait(&o_free[w], (oc - 1) & 1, kQSiteMmaO);
-          ++oc;
-        }
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t da = sdesc_add(dV, vs * C::TILE);
-        const uint64_t db = sdesc_add(dP, (w * C::PB + (e >> 1) % C::PB) * C::PBUF);
-        if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ss(tbase + C::O_COL(w), sdesc_add(da, kk * 2048),
-                  sdesc_add(db, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_o, (kk > 0 || !new_item) ? 1u : 0u);
-        umma_commit(&o_done[C::SHARE_V ? vs : w]);
-        if (!C::SHARE_V) umma_commit(&v_empty[vs]);
-        }
-        ++e;
-        if (++vs == C::VS) vs = 0, vpar ^= 1;
       }
-      if (leader) umma_commit(&drain);
+      // Every product issued completes before tensor memory is released.
+      uint64_t* end = warp == 9 ? &drain : &drain_pv;
+      if (leader) umma_commit(end);
       volatile int no_abort = 0;
       WaitCtl dw{p.status, &no_abort, p.wait_ns};
-      mbar_wait(&drain, 0, dw, kQSiteMmaDrain);
+      mbar_wait(end, 0, dw, kQSiteMmaDrain);
     } else if (lane == 0) {
       // ---------------------------------------------------------------- MMA issuer (warp 9)
       // One loop over the key tiles of all items.  Step j issues P V of its own tile and S of
@@ -1078,6 +1108,9 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           else tmem_ld32(tmem_addr(tbase, lb, b * N), sr);
           tmem_wait_ld();
           reg_fence(sr);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[b]);
         }
         const int kc0 = (j0 + s) * 128, key = kc0 + r;
         const bool masked = kc0 + 127 > sure_hi || kc0 < sure_lo;

@@ -717,10 +717,11 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             pg = p.num_blocks;  // outside the map: reads as zeros
           }
           __syncwarp();
-#pragma unroll 1
+          const bool leader = elect_one();
+#pragma unroll 4
           for (int i = i0; i < i0 + n; ++i) {
             const int page = __shfl_sync(0xffffffffu, pg, i);
-            if (lane == 0) {
+            if (leader) {
 #pragma unroll
               for (int c = 0; c < C::KCH; ++c)
                 tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64, row, it.kvh, page);

@@ -105,7 +105,7 @@ fa2_paged_tables_kernel(const TablesParams p) {
         }
       }
       p.positions[t] = pos;
-      p.slots[t] = block < 0 ? -1 : block * bs + pos - k * bs;
+      p.slots[t] = block < 0 || block > 0x7fffffff / bs - 1 ? -1 : block * bs + pos - k * bs;
     }
     cu0 += ta;
     take0 += tb;

@@ -115,17 +115,19 @@ fa2::SeqParams seq_params(const fa2_packed* O, float* LSE, const int* cu, unsign
 }
 
 // Form of a paged call's items, by the rows that the requests bring on average: two query
-// tiles of 128 rows (prompts, chunks), one, or 32 or 16 rows with the products' operands
-// swapped (decode steps; d <= 128).  Every form is right for every batch.
+// tiles of 128 rows (prompts, chunks), one, or 16 rows with the products' operands swapped
+// (decode steps; d <= 128).  Every form is right for every batch.  Measured on B200, caches of
+// 6k tokens, 16 rows -> one tile: d = 64: 1 row 171 -> 237 us, 4 rows 184 -> 237, 16 rows 179
+// -> 196; d = 128: 268 -> 301, 270 -> 302, 233 -> 251 us.  (The swapped form with 32 rows spilled
+// and took 660 us, one tile 203: it was dropped.)
 int paged_form(int B, int T, int G, int d) {
   if (d > 128) return 1;
   const long long rows = static_cast<long long>(T) * G, b = B;
   if (G <= 16 && rows <= 16 * b) return 16;
-  if (G <= 32 && rows <= 32 * b) return 32;
   return T > 128 / G * b ? 2 : 1;
 }
 int form_tiles(int form) { return form == 2 ? 2 : 1; }           // 128-row tiles of a partial slot
-int form_tokens(int form, int G) { return (form > 2 ? form : 128) / G; }  // tokens to a tile
+int form_tokens(int form, int G) { return (form == 16 ? 16 : 128) / G; }  // tokens to a tile
 
 // Float partials of the shares, two slots each: O, then LSE, then what is to be merged.
 size_t paged_opart_bytes(int grid, int qt, int d) {
@@ -298,6 +300,10 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
       static_cast<long long>(num_blocks) * block_size > 0x7fffffffll ||
       static_cast<long long>(max_blocks) * block_size > (1ll << 30))
     return FA2_ERR_INVALID_ARG;
+  // Blocks of rows times key tiles, which the kernel counts in 32 bits.
+  const int G = H / Hkv, form = paged_form(B, T, G, d), tpt = form_tokens(form, G);
+  if ((T / tpt + static_cast<long long>(B)) * (static_cast<long long>(max_blocks) * block_size / 128 + 4) > (1ll << 30))
+    return FA2_ERR_INVALID_ARG;
   if (T == 0) return FA2_OK;
   if (!packed_ok(Q, T, H, d) || !packed_ok(O, T, H, d) || !cache_ok(K, num_blocks, Hkv, block_size, d) ||
       !cache_ok(V, num_blocks, Hkv, block_size, d))
@@ -315,7 +321,6 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, n_sm))
     return FA2_ERR_WORKSPACE;
-  const int G = H / Hkv, form = paged_form(B, T, G, d), tpt = form_tokens(form, G);
   fa2::SeqMaps m;
   if (!map_packed(&m.q, Q, T, H, d, dtype, false, tpt, G) ||
       !map_cache(&m.k, K, num_blocks, Hkv, block_size, d, dtype) ||

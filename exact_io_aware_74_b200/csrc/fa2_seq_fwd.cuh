@@ -57,13 +57,13 @@ struct SeqParams {
   float scale_log2;
 };
 
-// NQ = 0: the layout above.  NQ = 16 or 32 (QT = 1): items of at most NQ rows, with the
+// NQ = 0: the layout above.  NQ = 16 (QT = 1): items of at most NQ rows, with the
 // operands of both products swapped (see the few-rows roles of the kernel).
 template <int D_, int QT_, int NQ_ = 0>
 struct SeqCfg {
   static constexpr int D = D_, QT = QT_, NQ = NQ_;
   static_assert(QT == 1 || D <= 128, "two accumulators fit tensor memory up to D = 128");
-  static_assert(NQ == 0 || (QT == 1 && D <= 128 && (NQ == 16 || NQ == 32)), "few rows");
+  static_assert(NQ == 0 || (QT == 1 && D <= 128 && NQ == 16), "few rows");
   static constexpr int KCH = D / 64;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = 128 * D * 2;
@@ -79,7 +79,7 @@ struct SeqCfg {
   // Few rows: P^T of each warpgroup, two chunks of 64 keys, PB buffers each (with two a
   // warpgroup need not wait for its last product before it writes the next P).  (At D = 64 the V operand's
   // upper 64 rows are whatever lies 16 KB behind the tile: at least that much follows.)
-  static constexpr int PBUF = 2 * NQ * 128, PB = NQ == 16 && D == 64 ? 2 : 1;
+  static constexpr int PBUF = 2 * NQ * 128, PB = D == 64 ? 2 : 1;
   static constexpr bool SHARE_V = NQ && VS % 2 == 0;
   static_assert(NQ == 0 || PB == 1 || (SHARE_V && 2 * PB <= VS), "a product's barrier comes round after its P buffer");
   static constexpr int PREST = QS * QTILE + 2 * PB * PBUF;
@@ -405,7 +405,7 @@ struct BlockOrder {
       sum += n;
       most = max(most, n);
     }
-    n_blocks = __reduce_add_sync(0xffffffffu, sum);
+    n_blocks = min(static_cast<int>(__reduce_add_sync(0xffffffffu, sum)), T / R + B);  // (bad offsets: no more)
     max_blk = __reduce_max_sync(0xffffffffu, most);
     __syncwarp();
   }
@@ -1105,8 +1105,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         uint32_t sr[N];
         if (got) {
           tc_fence_after();
-          if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, b * N), sr);
-          else tmem_ld32(tmem_addr(tbase, lb, b * N), sr);
+          tmem_ld16(tmem_addr(tbase, lb, b * N), sr);
           tmem_wait_ld();
           reg_fence(sr);
           tc_fence_before();
@@ -1163,14 +1162,12 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
           if (s != s0) {
             uint32_t o[N];
-            if constexpr (N == 16) tmem_ld16(tmem_addr(tbase, lb, C::O_COL(w)), o);
-            else tmem_ld32(tmem_addr(tbase, lb, C::O_COL(w)), o);
+            tmem_ld16(tmem_addr(tbase, lb, C::O_COL(w)), o);
             tmem_wait_ld();
             reg_fence(o);
 #pragma unroll
             for (int n = 0; n < N; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
-            if constexpr (N == 16) tmem_st16(tmem_addr(tbase, lb, C::O_COL(w)), o);
-            else tmem_st32(tmem_addr(tbase, lb, C::O_COL(w)), o);
+            tmem_st16(tmem_addr(tbase, lb, C::O_COL(w)), o);
             tmem_wait_st();
             tc_fence_before();
           }
@@ -1237,13 +1234,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (n0 < rows) {
         uint32_t o0[H2], o1[H2];
         if (steps > 0) {
-          if constexpr (H2 == 8) {
-            tmem_ld8(tmem_addr(tbase, lb, C::O_COL(0) + n0), o0);
-            tmem_ld8(tmem_addr(tbase, lb, C::O_COL(1) + n0), o1);
-          } else {
-            tmem_ld16(tmem_addr(tbase, lb, C::O_COL(0) + n0), o0);
-            tmem_ld16(tmem_addr(tbase, lb, C::O_COL(1) + n0), o1);
-          }
+          tmem_ld8(tmem_addr(tbase, lb, C::O_COL(0) + n0), o0);
+          tmem_ld8(tmem_addr(tbase, lb, C::O_COL(1) + n0), o1);
           tmem_wait_ld();
           reg_fence(o0);
           reg_fence(o1);

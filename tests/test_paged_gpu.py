@@ -114,6 +114,14 @@ def test_head_groups(H, Hk):
     Step([300, 10], [70, 3], H, Hk, 64, 64, "bf16", seed=H + 1).check(True, 100)
 
 
+@pytest.mark.parametrize("H,Hk", [(16, 1), (17, 1), (24, 1), (64, 2)])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (64, "fp16"), (128, "bf16"), (128, "fp16")])
+def test_rows_of_single_tokens(H, Hk, d, dtype):
+    """Decode steps with as many rows to an item as its forms hold, or just more."""
+    Step([300, 1500, 0, 127], [1, 1, 1, 1], H, Hk, d, 16, dtype, seed=H + d).check()
+    Step([900, 3], [2, 2], H, Hk, d, 64, dtype, seed=H + d + 1).check(True, 200)
+
+
 def test_many_requests():
     r = random.Random(3)
     n = 300

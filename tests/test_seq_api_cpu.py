@@ -106,6 +106,7 @@ def paged(lib, q=rows(1), k=pages(2), v=pages(3), o=rows(4), lse=5 * P, cu=6 * P
 
 @pytest.mark.parametrize("kw,expect", BAD_SIZES + BAD_MODES + [
     (dict(d=264), U), (dict(block=0), E), (dict(block=4), E), (dict(block=24), E), (dict(block=160), E),
+    (dict(T=1 << 22, H=256, Hk=2, most=1 << 20), E),  # more than the kernel counts
     (dict(blocks=0), E), (dict(most=0), E), (dict(blocks=1 << 28, block=16), E), (dict(most=1 << 27), E),
     (dict(k=pages(0)), E), (dict(v=pages(3, row=8)), E), (dict(k=pages(2, head=1001)), E), (dict(lens=0), E),
     (dict(table=0), E), (dict(table=P + 1), E), (dict(o=rows(2)), E), (dict(o=rows(1)), E),

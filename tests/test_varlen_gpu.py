@@ -339,3 +339,22 @@ def test_a_batch_of_no_rows():
     assert fa2.fa2_fwd_varlen(q, k, v, o, lse, cu, 0.1, True) == fa2.FA2_OK
     ok()
     assert (o == 7).all() and (lse == 7).all()
+    grads = [torch.full_like(x, 7).contiguous() for x in (q, k, v)]
+    ws = torch.empty(fa2.fa2_bwd_varlen_workspace_size(2, 40, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    assert fa2.fa2_bwd_varlen(q, k, v, o, do, lse, *grads, cu, ws, 0.1, True) == fa2.FA2_OK
+    ok()
+    assert all((x == 7).all() for x in grads)
+
+
+def test_bad_offsets_stay_inside_the_tensors():
+    """Offsets that fall, repeat or leave the tensors: nothing outside is touched (the results
+    are unspecified)."""
+    q, k, v, do, _ = make([300], 4, 2, 64, "bf16", 15)
+    buf = torch.full((302, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, lse = buf[1:301], torch.zeros((4, 300), device="cuda")
+    for at in ([0, 300, 0, 300], [-5, 100, 2 ** 31 - 1, 40], [290, 20, 300, -2 ** 31], [0, 300, 300, 300]):
+        cu = torch.tensor(at, dtype=torch.int32, device="cuda")
+        assert fa2.fa2_fwd_varlen(q, k, v, o, lse, cu, 0.1, True) == fa2.FA2_OK
+        fa2.backward_varlen(q, k, v, o, do, lse, cu, 0.1, True)
+        ok()
+        assert (buf[0] == 7).all() and (buf[301] == 7).all()

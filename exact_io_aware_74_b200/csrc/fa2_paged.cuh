@@ -26,10 +26,15 @@ struct TablesParams {
 
 constexpr int kTablesThreads = 512;
 
+// Blocks that hold n >= 0 tokens; n + bs - 1 may pass 2^31.
+__device__ __forceinline__ int blocks_for(int n, int bs) { return n > 0 ? (n - 1) / bs + 1 : 0; }
+
 // Every CTA sums the lengths of all requests (a block scan per 512 of them) and then
 // writes the table rows of every gridDim-th request and the slots of its own stretch
 // of tokens.  No CTA waits for another: a slot whose block is new in this step is taken
 // from the free list again rather than from the table entry that another CTA writes.
+// Sums past 2^31 give unspecified tables, but every index below is checked or clamped, so
+// that none reads or writes outside them.
 __global__ void __launch_bounds__(kTablesThreads)
 fa2_paged_tables_kernel(const TablesParams p) {
   __shared__ int s_ctx[kTablesThreads], s_cu[kTablesThreads + 1], s_first[kTablesThreads];
@@ -42,8 +47,8 @@ fa2_paged_tables_kernel(const TablesParams p) {
   for (int r0 = 0; r0 < p.B; r0 += kTablesThreads) {
     const int r = r0 + tid;
     const int ctx = r < p.B ? max(0, p.context_lens[r]) : 0;
-    const int nw = r < p.B ? max(0, p.new_lens[r]) : 0;
-    const int had = (ctx + bs - 1) / bs, need = (ctx + nw + bs - 1) / bs;
+    const int nw = r < p.B ? min(max(0, p.new_lens[r]), 0x7fffffff - ctx) : 0;
+    const int had = blocks_for(ctx, bs), need = blocks_for(ctx + nw, bs);
     int a = nw, b = need - had;  // inclusive sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -77,16 +82,16 @@ fa2_paged_tables_kernel(const TablesParams p) {
     // Table rows: a warp to a request, every gridDim-th of them here.
     for (int i = warp; i < cnt; i += kTablesThreads / 32) {
       if ((r0 + i) % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) continue;
-      const int c = s_ctx[i], n = s_cu[i + 1] - s_cu[i];
-      const int h = (c + bs - 1) / bs, e = min(p.max_blocks, (c + n + bs - 1) / bs);
+      const int c = s_ctx[i], n = min(max(s_cu[i + 1] - s_cu[i], 0), 0x7fffffff - c);
+      const int h = blocks_for(c, bs), e = min(p.max_blocks, blocks_for(c + n, bs));
       int* row = p.block_table + static_cast<size_t>(r0 + i) * p.max_blocks;
-      for (int k = h + lane; k < e; k += 32) {
-        const int f = s_first[i] + k;
-        row[k] = f < p.num_free ? p.free_blocks[f] : -1;
+      for (long long k = static_cast<long long>(h) + lane; k < e; k += 32) {  // (h + lane may pass 2^31)
+        const int f = s_first[i] + static_cast<int>(k);
+        row[k] = f >= 0 && f < p.num_free ? p.free_blocks[f] : -1;
       }
     }
     // Tokens of this CTA's stretch that belong to these requests.
-    const int lo = max(t_lo, cu0), hi = min(t_hi, cu0 + ta);
+    const int lo = min(t_hi, max(t_lo, cu0)), hi = min(t_hi, cu0 + ta);
     for (int t = lo + tid; t < hi; t += kTablesThreads) {
       int i = 0, j = cnt;  // the last request that starts at or before t
       while (j - i > 1) {
@@ -96,12 +101,12 @@ fa2_paged_tables_kernel(const TablesParams p) {
       const int c = s_ctx[i], pos = c + t - s_cu[i];
       const int k = pos / bs;
       int block = -1;
-      if (k < p.max_blocks) {
-        if (k < (c + bs - 1) / bs) {
+      if (pos >= 0 && k < p.max_blocks) {
+        if (k < blocks_for(c, bs)) {
           block = p.block_table[static_cast<size_t>(r0 + i) * p.max_blocks + k];
         } else {
           const int f = s_first[i] + k;
-          if (f < p.num_free) block = p.free_blocks[f];
+          if (f >= 0 && f < p.num_free) block = p.free_blocks[f];
         }
       }
       p.positions[t] = pos;
@@ -111,7 +116,7 @@ fa2_paged_tables_kernel(const TablesParams p) {
     take0 += tb;
     __syncthreads();  // the shared sums are rewritten
   }
-  for (int t = max(t_lo, cu0) + tid; t < t_hi; t += kTablesThreads) {
+  for (int t = min(t_hi, max(t_lo, cu0)) + tid; t < t_hi; t += kTablesThreads) {
     p.positions[t] = 0;
     p.slots[t] = -1;
   }

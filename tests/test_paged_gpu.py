@@ -281,6 +281,41 @@ def test_tables_count_negative_lengths_as_none():
     assert [x.tolist() for x in got] == [[[8, 0], [4, 0]], [0, 2, 2], [2, 5], [0, 1, 0], [32, 33, -1], [1]]
 
 
+def test_tables_of_lengths_up_to_31_bits():
+    """Lengths whose rounding up to whole blocks passes 2^31; the table keeps what it held."""
+    top = 2 ** 31 - 1
+    for context, new in (([top - 20, 5], [20, 3]), ([top, 0], [0, 9]), ([top - 3, top], [3, 0])):
+        for block in (16, 1, 1000):
+            table = [[7, 8], [9, 10]]
+            free = list(range(100, 120))
+            got = fa2.paged_tables(ints(context), ints(new), ints(free), ints(table), sum(new) + 2, block)
+            ok()
+            taken = -(-(context[0] + new[0]) // block) - -(-context[0] // block)
+            for i in range(-(-context[1] // block), min(2, -(-(context[1] + new[1]) // block))):
+                k = taken + i - -(-context[1] // block)
+                table[1][i] = free[k] if k < len(free) else -1
+            assert got[0].tolist() == table
+            assert got[2].tolist() == [c + n for c, n in zip(context, new)]
+            at = [c + i for c, n in zip(context, new) for i in range(n)]
+            assert got[3].tolist() == at + [0, 0]
+            assert got[4].tolist()[:new[0]] == [-1] * new[0] and got[4].tolist()[-2:] == [-1, -1]
+
+
+def test_tables_of_sums_past_31_bits_stay_inside():
+    """The results are unspecified; nothing outside the tables is touched."""
+    top = 2 ** 31 - 1
+    for context, new in (([0, 0, 0], [top, top, top]), ([top, top, 5], [top, 9, top]), ([1, 2, 3], [2 ** 30] * 3)):
+        buf = ints([[7] * 4] * 5)
+        out = ints([7] * 12)
+        positions, slots = ints([7] * 12), ints([7] * 12)
+        assert fa2.fa2_paged_tables(ints(context), ints(new), ints([1, 2, 3]), buf[1:4], out[1:5], out[6:9],
+                                    positions[1:11], slots[1:11], out[10:11], 16) == fa2.FA2_OK
+        ok()
+        assert (buf[0] == 7).all() and (buf[4] == 7).all()
+        assert [int(out[i]) for i in (0, 5, 9, 11)] == [7] * 4
+        assert [int(x[i]) for x in (positions, slots) for i in (0, 11)] == [7] * 4
+
+
 # ------------------------------------------------------------------ append
 
 @pytest.mark.parametrize("T", [1, 7, 300])

@@ -8,6 +8,7 @@ missing or unloadable library raises ``RuntimeError`` -- there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -340,6 +341,22 @@ def _call(fn, dev: int, stream, *args) -> int:
         return fn(*args, raw)
 
 
+def _c_int(x) -> int:
+    """A window or block size as a C int: ctypes would take it modulo 2^32."""
+    return max(-1, min(x, 0x7fffffff))
+
+
+def _home(t, stream):
+    """Context in which outputs and workspaces of a call on ``stream`` are allocated: on that
+    stream, so that their memory is free there when the call writes it and is not handed out
+    to another stream while the call still runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
 def _bytes(workspace, dev: int) -> tuple[int | None, int]:
     if workspace is None:
         return None, 0
@@ -360,7 +377,7 @@ def fa2_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale: float, causal: bool, wind
                  _rows("k", k, (T, Hkv, d), dt, dev), _rows("v", v, (T, Hkv, d), dt, dev),
                  _rows("o", o, shape, dt, dev), _lse(lse, H, T, dev),
                  _ints("cu_seqlens", cu_seqlens, n, dev), n - 1, T, H, Hkv, d, scale,
-                 1 if causal else 0, window, code)
+                 1 if causal else 0, _c_int(window), code)
 
 
 def fa2_bwd_varlen_workspace_size(B: int, T: int, H: int, Hkv: int, d: int) -> int:
@@ -381,7 +398,7 @@ def fa2_bwd_varlen(q, k, v, o, do, lse, dq, dk, dv, cu_seqlens, workspace, scale
                  _lse(lse, H, T, dev), _rows("dq", dq, shape, dt, dev),
                  _rows("dk", dk, kv, dt, dev), _rows("dv", dv, kv, dt, dev),
                  _ints("cu_seqlens", cu_seqlens, n, dev), *_bytes(workspace, dev), n - 1, T, H,
-                 Hkv, d, scale, 1 if causal else 0, window, code)
+                 Hkv, d, scale, 1 if causal else 0, _c_int(window), code)
 
 
 def fa2_fwd_paged_workspace_size(B: int, T: int, H: int, Hkv: int, d: int,
@@ -404,7 +421,7 @@ def fa2_fwd_paged(q, k_cache, v_cache, o, lse, block_table, cu_seqlens, seq_lens
                  _lse(lse, H, T, dev), _ints("cu_seqlens", cu_seqlens, B + 1, dev),
                  _ints("seq_lens", seq_lens, B, dev),
                  _ints("block_table", block_table, B * most, dev), *_bytes(workspace, dev), B, T,
-                 H, Hkv, d, blocks, bs, most, scale, 1 if causal else 0, window, code)
+                 H, Hkv, d, blocks, bs, most, scale, 1 if causal else 0, _c_int(window), code)
 
 
 def fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu_seqlens, seq_lens,
@@ -421,7 +438,7 @@ def fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu_seqlen
                  _ints("block_table", block_table, B * most, dev),
                  _ints("cu_seqlens", cu_seqlens, B + 1, dev), _ints("seq_lens", seq_lens, B, dev),
                  _ints("positions", positions, T, dev), _ints("slots", slots, T, dev),
-                 _ints("used", used, 1, dev), B, T, block_size, most)
+                 _ints("used", used, 1, dev), B, T, _c_int(block_size), most)
 
 
 def fa2_paged_append(k, v, k_cache, v_cache, slots, stream=None) -> int:
@@ -464,6 +481,10 @@ def fa2_launch_count() -> int:
 
 # ------------------------------------------------------------------------------------
 # allocating conveniences (PyTorch owns the memory)
+#
+# Those of the packed and paged calls allocate on the stream that they are given; to use
+# or free their outputs on another one, order the two streams as for any tensor (wait_stream,
+# record_stream).
 # ------------------------------------------------------------------------------------
 
 def forward(q, k, v, scale: float, causal: bool, stream=None):
@@ -560,8 +581,9 @@ def forward_varlen(q, k, v, cu_seqlens, scale: float, causal: bool, window: int 
     [T,Hkv,d], sequence b being rows cu_seqlens[b] .. cu_seqlens[b+1] - 1.  Rows behind
     the last sequence are not written (fa2_fwd_varlen takes outputs of your own)."""
     T, H, d = _dims("q", q, 3)
-    o = q.new_empty((T, H, d))
-    lse = q.new_empty((H, T), dtype=torch.float32)
+    with _home(q, stream):
+        o = q.new_empty((T, H, d))
+        lse = q.new_empty((H, T), dtype=torch.float32)
     rc = fa2_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, window, stream)
     if rc != FA2_OK:
         raise FA2Error(rc, "fa2_fwd_varlen")
@@ -574,11 +596,12 @@ def backward_varlen(q, k, v, o, do, lse, cu_seqlens, scale: float, causal: bool,
     allocated if not given."""
     T, H, d = _dims("q", q, 3)
     Hkv = _dims("k", k, 3)[1]
-    if workspace is None:
-        n = fa2_bwd_varlen_workspace_size(cu_seqlens.numel() - 1, T, H, Hkv, d)
-        workspace = q.new_empty(n, dtype=torch.uint8)
-    dq = q.new_empty((T, H, d))
-    dk, dv = q.new_empty((T, Hkv, d)), q.new_empty((T, Hkv, d))
+    with _home(q, stream):
+        if workspace is None:
+            n = fa2_bwd_varlen_workspace_size(cu_seqlens.numel() - 1, T, H, Hkv, d)
+            workspace = q.new_empty(n, dtype=torch.uint8)
+        dq = q.new_empty((T, H, d))
+        dk, dv = q.new_empty((T, Hkv, d)), q.new_empty((T, Hkv, d))
     rc = fa2_bwd_varlen(q, k, v, o, do, lse, dq, dk, dv, cu_seqlens, workspace, scale, causal,
                         window, stream)
     if rc != FA2_OK:
@@ -597,12 +620,13 @@ def forward_paged(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scale:
     [blocks,Hkv,block_size,d]: O [T,H,d] and LSE [H,T].  The workspace is allocated if
     not given."""
     T, H, d = _dims("q", q, 3)
-    if workspace is None:
-        n = fa2_fwd_paged_workspace_size(block_table.shape[0], T, H, k_cache.shape[1], d,
-                                         _sm_count(_device_of(q)))
-        workspace = q.new_empty(n, dtype=torch.uint8)
-    o = q.new_empty((T, H, d))
-    lse = q.new_empty((H, T), dtype=torch.float32)
+    B, Hkv = _dims("block_table", block_table, 2)[0], _dims("k_cache", k_cache, 4)[1]
+    with _home(q, stream):
+        if workspace is None:
+            n = fa2_fwd_paged_workspace_size(B, T, H, Hkv, d, _sm_count(_device_of(q)))
+            workspace = q.new_empty(n, dtype=torch.uint8)
+        o = q.new_empty((T, H, d))
+        lse = q.new_empty((H, T), dtype=torch.float32)
     rc = fa2_fwd_paged(q, k_cache, v_cache, o, lse, block_table, cu_seqlens, seq_lens, workspace,
                        scale, causal, window, stream)
     if rc != FA2_OK:
@@ -614,9 +638,11 @@ def paged_tables(context_lens, new_lens, free_blocks, block_table, T: int, block
                  stream=None):
     """Tables of a step of at most T new tokens: (block_table, updated in place,
     cu_seqlens [B+1], seq_lens [B], positions [T], slots [T], used [1])."""
-    B = block_table.shape[0]
-    empty = block_table.new_empty
-    cu, lens, positions, slots, used = empty(B + 1), empty(B), empty(T), empty(T), empty(1)
+    B = _dims("block_table", block_table, 2)[0]
+    with _home(block_table, stream):
+        # one allocation for the five: their time is most of the call's
+        cu, lens, positions, slots, used = block_table.new_empty(2 * B + 2 * T + 2).split(
+            (B + 1, B, T, T, 1))
     rc = fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu, lens, positions,
                           slots, used, block_size, stream)
     if rc != FA2_OK:

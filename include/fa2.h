@@ -329,8 +329,8 @@ typedef struct {
  *   T          : >= 0 (0 launches nothing); d a multiple of 8 up to 256
  *   window     : 0, or >= 1 with causal = 1
  * What lies in the tensors outside the sequences (NaN included) does not reach them.
- * O and LSE must not overlap the inputs (FA2_ERR_INVALID_ARG when O or LSE start inside
- * one).  Results are bitwise repeatable.
+ * O and LSE must not overlap the inputs (FA2_ERR_INVALID_ARG when one starts where an
+ * input does).  Results are bitwise repeatable.
  */
 int fa2_fwd_varlen(const fa2_packed* Q, const fa2_packed* K, const fa2_packed* V,
                    const fa2_packed* O, float* LSE, const int* cu_seqlens, int B, int T, int H,

@@ -417,6 +417,35 @@ def test_serving_steps(H, Hk, d, block, window, graph):
     _serve(STEPS, H, Hk, d, block, window, graph)
 
 
+def test_steps_on_a_stream_that_is_not_the_current_one():
+    """A call on a given stream, its outputs and workspace allocated by it, while the current
+    stream allocates and fills tensors of the same sizes."""
+    s = Step([3000, 700, 0, 90], [1, 40, 130, 1], 8, 2, 128, 16, "bf16", seed=30)
+    ref = s.run()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    need = fa2.fa2_fwd_paged_workspace_size(4, s.q.shape[0], 8, 2, 128)
+    for stream in (st, st.cuda_stream):
+        outs = []
+        for _ in range(6):
+            outs.append(fa2.forward_paged(s.q, s.k_cache, s.v_cache, s.table, s.cu, s.lens, s.scale, True,
+                                          stream=stream))
+            torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+            torch.full_like(s.q, 3)
+        st.synchronize()
+        for o, lse in outs:
+            assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    ok()
+
+
+def test_a_window_past_32_bits_hides_nothing():
+    s = Step([300, 5], [1, 70], 4, 2, 64, 16, "bf16", seed=31)
+    full = s.run()
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5):
+        got = s.run(True, window)
+        assert all(torch.equal(a, b) for a, b in zip(got, full))
+
+
 def test_prompts_through_the_cache_agree_with_the_packed_forward():
     """Whole prompts written to the cache and read back are the packed prompts."""
     lens, H, Hk, d, block = [200, 1, 77], 8, 2, 128, 16

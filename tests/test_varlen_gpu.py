@@ -306,6 +306,39 @@ def test_two_streams_at_once():
     ok()
 
 
+def test_calls_on_a_stream_that_is_not_the_current_one():
+    """Outputs and workspace allocated by the call belong to its stream: tensors of their sizes
+    that the current stream allocates and fills meanwhile are others."""
+    q, k, v, do, cu = make([300, 90, 1, 700], 4, 2, 64, "bf16", 16)
+    o, lse = fa2.forward_varlen(q, k, v, cu, 0.1, True)
+    g = fa2.backward_varlen(q, k, v, o, do, lse, cu, 0.1, True)
+    need = fa2.fa2_bwd_varlen_workspace_size(4, q.shape[0], 4, 2, 64)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(5):
+        o2, lse2 = fa2.forward_varlen(q, k, v, cu, 0.1, True, stream=st)
+        outs.append((o2, lse2) + fa2.backward_varlen(q, k, v, o2, do, lse2, cu, 0.1, True, stream=st))
+        torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        torch.full_like(do, 3)
+    st.synchronize()
+    for got in outs:
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+        assert torch.equal(got[3], g[1]) and torch.equal(got[4], g[2])
+        # dQ: sums of at most six 32-bit partials in another order, then one rounding each
+        assert ((got[2].float() - g[0].float()).abs() <= 2 ** -7 * g[0].float().abs() + 1e-5).all()
+    ok()
+
+
+def test_a_window_past_32_bits_hides_nothing():
+    q, k, v, _, cu = make([300, 5], 4, 2, 64, "bf16", 17)
+    full = fa2.forward_varlen(q, k, v, cu, 0.1, True)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5):
+        got = fa2.forward_varlen(q, k, v, cu, 0.1, True, window)
+        assert all(torch.equal(a, b) for a, b in zip(got, full))
+    ok()
+
+
 def test_row_offsets_past_32_bits():
     """Rows so far apart that element offsets pass 2^32."""
     H, Hk, d, T = 2, 1, 64, 70000

@@ -300,9 +300,11 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
       static_cast<long long>(num_blocks) * block_size > 0x7fffffffll ||
       static_cast<long long>(max_blocks) * block_size > (1ll << 30))
     return FA2_ERR_INVALID_ARG;
-  // Blocks of rows times key tiles, which the kernel counts in 32 bits.
+  // Blocks of rows times key tiles times heads, which the kernel counts in 32 bits.  (The first
+  // factors stay below 2^30 and 2^24.)
   const int G = H / Hkv, form = paged_form(B, T, G, d), tpt = form_tokens(form, G);
-  if ((T / tpt + static_cast<long long>(B)) * (static_cast<long long>(max_blocks) * block_size / 128 + 4) > (1ll << 30))
+  const long long row_blocks = T / (tpt * form_tiles(form)) + static_cast<long long>(B);
+  if (row_blocks * (static_cast<long long>(max_blocks) * block_size / 128 + 6) > (1ll << 30) / Hkv)
     return FA2_ERR_INVALID_ARG;
   if (T == 0) return FA2_OK;
   if (!packed_ok(Q, T, H, d) || !packed_ok(O, T, H, d) || !cache_ok(K, num_blocks, Hkv, block_size, d) ||
@@ -331,7 +333,8 @@ int fa2_fwd_paged(const fa2_packed* Q, const fa2_cache* K, const fa2_cache* V, c
   p.seq_lens = seq_lens;
   p.block_table = block_table;
   p.num_blocks = num_blocks, p.block_size = block_size, p.max_blocks = max_blocks;
-  p.box_rows = std::min(block_size, 128);
+  p.tiles_block = block_size / 128;
+  for (p.box_shift = 3; 1 << p.box_shift < std::min(block_size, 128);) ++p.box_shift;
   p.O_part = static_cast<float*>(workspace);
   p.LSE_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_opart_bytes(n_sm, form_tiles(form), d));
   p.merge = reinterpret_cast<int4*>(p.LSE_part + static_cast<size_t>(n_sm) * 2 * form_tiles(form) * 128);

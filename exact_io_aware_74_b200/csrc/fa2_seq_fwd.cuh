@@ -53,7 +53,7 @@ struct SeqParams {
   int B, T, Hkv, G, d, tpt;  // tpt: tokens to a tile, 128 / G
   int causal, window, fault, head_group;
   int num_blocks, block_size, max_blocks;
-  int box_rows;  // paged: rows of a box, min(block_size, 128)
+  int box_shift, tiles_block;  // paged: rows of a box, min(block_size, 128), are 1 << box_shift; key tiles to a block
   float scale_log2;
 };
 
@@ -181,26 +181,25 @@ __device__ __forceinline__ void cut_item(SeqItem& it, int a, int e) {
 }
 
 // Units of work of block blk of a sequence: its key tiles (both query tiles' together, at
-// least one) and kItemUnits for its start and end, which come first in the linear order.
-// (An item of two query tiles costs about 5 us beside 2.6 us a key tile.  With key tiles
-// alone the share with a prompt's many short blocks ended at 300 us, the others at 175.)
-template <int QT>
-constexpr int kItemUnits = QT == 2 ? 2 : 1;
-template <int QT>
+// least one) and IU for its start and end, which come first in the linear order.  (With key
+// tiles alone the share with a prompt's many short blocks ended at 300 us, the others at 175;
+// the shares of a decode step ended between 180 and 233 us with one unit to an item.)
+constexpr int kItemUnits = 4;
+template <int QT, int IU>
 __device__ __forceinline__ int block_units(const SeqParams& p, int n, int nk, int blk) {
   const int a = blk * (QT * p.tpt);
   int lo, hi;
   key_range(p, SeqLen{0, n, nk}, a, min(n, a + QT * p.tpt), lo, hi);
-  return max(1, hi - lo) + kItemUnits<QT>;
+  return max(1, hi - lo) + IU;
 }
 __device__ __forceinline__ int blocks_of(int n, int R) { return n <= R ? (n > 0) : (n + R - 1) / R; }
 
 // Units of one key/value head of a sequence per lane: of a single block each lane its own,
 // of more the whole warp together.
-template <int QT>
+template <int QT, int IU>
 __device__ __forceinline__ int lane_units(const SeqParams& p, int n, int nk, int lane) {
   const int R = QT * p.tpt;
-  int u = n > 0 ? block_units<QT>(p, n, nk, 0) : 0;
+  int u = n > 0 ? block_units<QT, IU>(p, n, nk, 0) : 0;
   unsigned int many = __ballot_sync(0xffffffffu, n > R);
 #pragma unroll 1
   while (many) {
@@ -209,7 +208,7 @@ __device__ __forceinline__ int lane_units(const SeqParams& p, int n, int nk, int
     const int on = __shfl_sync(0xffffffffu, n, l), ok = __shfl_sync(0xffffffffu, nk, l);
     int part = 0;
 #pragma unroll 1
-    for (int i = lane; i * R < on; i += 32) part += block_units<QT>(p, on, ok, i);
+    for (int i = lane; i * R < on; i += 32) part += block_units<QT, IU>(p, on, ok, i);
     part = __reduce_add_sync(0xffffffffu, part);
     if (lane == l) u = part;
   }
@@ -226,12 +225,11 @@ __device__ __forceinline__ int warp_inclusive(int x, int lane) {
 }
 
 // Units to a share: equal for `grid` CTAs (the last ones may get fewer or none), at least
-// kMinUnits.  32-bit division wherever it will do: this is the first code that every CTA
-// runs, from a cold instruction cache.
+// kMinUnits.  All units together are below 2^31 (checked by the caller): 64-bit divisions
+// alone were 7 KB of code.
 constexpr int kMinUnits = 2;
-__device__ __forceinline__ long long share_units(long long total, int grid) {
-  if (total < (1ll << 31)) return max((static_cast<unsigned int>(total) + grid - 1) / static_cast<unsigned int>(grid), kMinUnits + 0u);
-  return static_cast<long long>(static_cast<unsigned int>(total >> 16) / static_cast<unsigned int>(grid) + 1) << 16;
+__device__ __forceinline__ int share_units(int total, int grid) {
+  return max((static_cast<unsigned int>(total) + grid - 1) / static_cast<unsigned int>(grid), kMinUnits + 0u);
 }
 
 // The linear order of the units: sequence, head, block, key tile.  Whole warp.
@@ -242,10 +240,10 @@ struct UnitAt {
 
 // Finds share c: units x .. xe - 1, `per` to a share.  False when there is none.  held:
 // kHeld ints of shared memory.  One loop body serves the total and the search.
-template <int QT>
-__device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, int* held, int lane, long long& per,
-                                           long long& x, long long& xe, UnitAt& r) {
-  long long total = 0, rem = 0;
+template <int QT, int IU>
+__device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, int* held, int lane, int& per, int& x, int& xe,
+                                           UnitAt& r) {
+  int total = 0, rem = 0;
   int units = 1;  // of one head of the sequence found
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -257,11 +255,11 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
       } else {
         SeqLen s{0, 0, 0};
         if (b0 + lane < p.B) s = seq_len<true>(p, b0 + lane);
-        v = lane_units<QT>(p, s.n, s.nk, lane);
+        v = lane_units<QT, IU>(p, s.n, s.nk, lane);
         if (b0 < kHeld) held[b0 + lane] = v;
       }
       const int inc = warp_inclusive(v, lane);
-      const long long end = static_cast<long long>(inc) * p.Hkv;
+      const int end = inc * p.Hkv;
       if (pass == 0) {
         total += __shfl_sync(0xffffffffu, end, 31);
         continue;
@@ -271,7 +269,7 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
         const int l = __ffs(m) - 1;
         r.b = b0 + l;
         units = __shfl_sync(0xffffffffu, v, l);
-        rem -= __shfl_sync(0xffffffffu, end, l) - static_cast<long long>(units) * p.Hkv;
+        rem -= __shfl_sync(0xffffffffu, end, l) - units * p.Hkv;
         break;
       }
       rem -= __shfl_sync(0xffffffffu, end, 31);
@@ -279,22 +277,20 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
     if (pass == 0) {
       per = share_units(total, grid);
       x = rem = per * c;
-      xe = min(total, x + per);
-      if (x >= total) return false;
+      if (x >= total || x < 0) return false;  // (per * c may pass 2^31)
+      xe = min(total - x, per) + x;
       __syncwarp();
     }
   }
   r.s = seq_len<true>(p, r.b);
-  // A sequence's units are below 2^31 for one head, its heads' together perhaps not.
-  r.kvh = rem < (1ll << 31) ? static_cast<unsigned int>(rem) / static_cast<unsigned int>(units)
-                            : static_cast<int>(rem / units);
-  int at = static_cast<int>(rem - static_cast<long long>(r.kvh) * units);
+  r.kvh = static_cast<unsigned int>(rem) / static_cast<unsigned int>(units);
+  int at = rem - r.kvh * units;
   const int R = QT * p.tpt, nb = blocks_of(r.s.n, R);
   r.blk = 0;
   if (nb > 1) {
 #pragma unroll 1
     for (int i0 = 0; i0 < nb; i0 += 32) {
-      const int v = i0 + lane < nb ? block_units<QT>(p, r.s.n, r.s.nk, i0 + lane) : 0;
+      const int v = i0 + lane < nb ? block_units<QT, IU>(p, r.s.n, r.s.nk, i0 + lane) : 0;
       const int inc = warp_inclusive(v, lane);
       const unsigned int m = __ballot_sync(0xffffffffu, inc > at);
       if (m) {
@@ -311,15 +307,15 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
 }
 
 // The items of one CTA's share, one after the other.  Whole warp.
-template <int QT>
+template <int QT, int IU>
 struct ShareWalk {
-  long long per, x, xe;  // units to a share; next unit, end
+  int per, x, xe;  // units to a share; next unit, end
   UnitAt u;
 
   __device__ __forceinline__ void start(const SeqParams& p, int* held, int lane) {
     const int c = blockIdx.x;
     if (lane == 0) p.merge[c] = make_int4(0, 0, 0, 0);  // nothing to merge, until a block is cut
-    if (!find_share<QT>(p, gridDim.x, c, held, lane, per, x, xe, u)) x = xe = 0;
+    if (!find_share<QT, IU>(p, gridDim.x, c, held, lane, per, x, xe, u)) x = xe = 0;
   }
   // The next item with key tiles; false at the end of the share.
   __device__ __forceinline__ bool next(const SeqParams& p, int lane, SeqItem& it) {
@@ -327,16 +323,16 @@ struct ShareWalk {
     bool found = false;
 #pragma unroll 1
     while (!found && x < xe) {
-      const int len = block_units<QT>(p, u.s.n, u.s.nk, u.blk);
-      const int take = static_cast<int>(min(static_cast<long long>(len - u.at), xe - x));
+      const int len = block_units<QT, IU>(p, u.s.n, u.s.nk, u.blk);
+      const int take = min(len - u.at, xe - x);
       make_item<true, QT>(p, u.s, u.b, u.kvh, u.blk, it);
       // Key tiles [a, e) of the block's fall into this share.
-      constexpr int C0 = kItemUnits<QT>;
-      const int a = max(0, u.at - C0), e = max(0, u.at + take - C0);
+      const int a = max(0, u.at - IU), e = max(0, u.at + take - IU);
       if (it.n == 0) {
         // Rows that see no key: O = 0 and LSE = -inf, here.  (The other roles then never meet
         // an item without key tiles, which would be in the way of the next one.)
         if (e > a)
+#pragma unroll 1
           for (int r = 0; r < it.n_tok * p.G; ++r) {
             const int row = it.row0 + r / p.G, head = u.kvh * p.G + r % p.G;
             if (lane * 8 < p.d)
@@ -345,11 +341,12 @@ struct ShareWalk {
           }
       } else if (e > a) {
         found = true;
-        if (a > 0 || e < len - C0) {
+        if (a > 0 || e < len - IU) {
           if (a == 0 && lane == 0) {
             // The block goes on in the next shares: for the merge kernel.
             int parts = 1;
-            for (long long end = xe; end < x + len - u.at; end += per) ++parts;
+#pragma unroll 1
+            for (int left = x + len - u.at - xe; left > 0; left -= per) ++parts;
             p.merge[c] = make_int4(it.row0, it.n_tok, u.kvh, parts);
           }
           cut_item(it, a, e);
@@ -507,7 +504,10 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
 // MMA issuer the not causal 2 x 32 x 8192 forward took 2590 us, not 2250): some thirty
 // copies of the loop are a quarter of the kernel's code, and what runs once an item then
 // misses the instruction cache (238 KB of code ran items of one key tile at 11 us, 127 KB at
-// 7 us; B200).
+// 7 us; B200).  For the same reason what runs once an item or seldom is not unrolled: on SMs
+// that had been through a few items, straight arithmetic of the softmax stalled for up to 2 us
+// a key tile.  With 88 instead of 112 KB (and 92 instead of 153 for few rows) a step of chunks
+// over 8k caches takes 195 us, not 227, the full decode step 219, not 232.
 static __device__ __noinline__ bool mbar_wait_loop(uint32_t bar, uint32_t parity, unsigned int* status,
                                                    volatile int* abort, uint64_t limit_ns, uint32_t site) {
   const uint64_t t0 = global_timer_ns();
@@ -630,7 +630,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       SeqItem it{};
       bool ok = true;
       if constexpr (PAGED) {
-        ShareWalk<QT> walk;
+        ShareWalk<QT, kItemUnits> walk;
         walk.start(p, held, lane);
         while (ok && walk.next(p, lane, it)) ok = publish(it);
       } else {
@@ -685,7 +685,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       unsigned int raw_par = 0;          // V: parity of the loads on v_raw, per slot
       int fix = -1, fix_a = 0, fix_e = 0;  // V: slot to be zeroed outside rows [fix_a, fix_e)
       bool ok = true, skip = p.fault == 1 && !is_v;  // test hook: the first K tile is not loaded
-      [[maybe_unused]] const int nbox = PAGED ? 128 / p.box_rows : 1;
+      [[maybe_unused]] const int bsh = p.box_shift, nbox = 128 >> bsh;  // rows of a box: 1 << bsh
       auto wait_all = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, mbar_wait_far(bar, par, wc, kQSiteProd)) != 0;
       };
@@ -693,8 +693,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       auto pages_of = [&](const SeqItem& it, int j) -> int {
         int a, e, pg = 0;
         tile_keys(it, j, a, e);
-        if (lane < nbox && lane * p.box_rows < e && (lane + 1) * p.box_rows > a) {
-          const int at = p.block_size <= 128 ? j * nbox + lane : j * 128 / p.block_size;
+        if (lane < nbox && lane << bsh < e && (lane + 1) << bsh > a) {
+          const int at = p.tiles_block <= 1 ? j * nbox + lane : j / p.tiles_block;
           pg = p.block_table[static_cast<size_t>(it.key0) * p.max_blocks + at];
         }
         return pg;  // not looked at here: the load goes on behind the tile before
@@ -709,22 +709,26 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         } else {
           int a, e;
           tile_keys(it, j, a, e);
-          const int i0 = a / p.box_rows, n = (e + p.box_rows - 1) / p.box_rows - i0;
-          const int row = p.block_size <= 128 ? 0 : j * 128 % p.block_size;
-          if (lane == 0) mbar_arrive_expect_tx(bar, n * p.box_rows * 128 * C::KCH);
+          const int i0 = a >> bsh, n = ((e + (1 << bsh) - 1) >> bsh) - i0;
+          const int row = p.tiles_block <= 1 ? 0 : j % p.tiles_block * 128;
+          if (lane == 0) mbar_arrive_expect_tx(bar, (n << bsh) * 128 * C::KCH);
           if (pg < 0 || pg >= p.num_blocks) {
             atomicCAS(p.status, 0u, kStatusInvalid | (kPSiteBlock << 8));
             pg = p.num_blocks;  // outside the map: reads as zeros
           }
           __syncwarp();
           const bool leader = elect_one();
-#pragma unroll 4
-          for (int i = i0; i < i0 + n; ++i) {
-            const int page = __shfl_sync(0xffffffffu, pg, i);
-            if (leader) {
+          // Four to a turn, without a remainder of its own (it was half of this code).
+#pragma unroll 1
+          for (int i = i0; i < i0 + n; i += 4) {
 #pragma unroll
-              for (int c = 0; c < C::KCH; ++c)
-                tma_load_4d(dst + c * C::CHUNK + i * p.box_rows * 128, map, bar, c * 64, row, it.kvh, page);
+            for (int k = 0; k < 4; ++k) {
+              const int page = __shfl_sync(0xffffffffu, pg, i + k);
+              if (leader && i + k < i0 + n) {
+#pragma unroll
+                for (int c = 0; c < C::KCH; ++c)
+                  tma_load_4d(dst + c * C::CHUNK + ((i + k) << bsh) * 128, map, bar, c * 64, row, it.kvh, page);
+              }
             }
           }
         }
@@ -733,8 +737,10 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (!wait_all(&v_raw[fix], raw_par >> fix & 1)) return false;
         raw_par ^= 1u << fix;
         uint8_t* v = sV + fix * C::TILE + (lane & 7) * 16;
+#pragma unroll 1
         for (int r = lane >> 3; r < 128; r += 4)
           if (r < fix_a || r >= fix_e)
+#pragma unroll
             for (int c = 0; c < C::KCH; ++c)
               *reinterpret_cast<uint4*>(v + c * C::CHUNK + r * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -752,6 +758,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (it.n == 0) continue;
         int pg = 0;
         if constexpr (PAGED) pg = pages_of(it, it.j0);
+#pragma unroll 1
         for (int jj = 0; jj < it.n && ok; ++jj) {
           const int j = it.j0 + jj;
           // Q: tile 0 ahead of the item's first K tile, tile 1 behind it.
@@ -776,12 +783,19 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           tile_keys(it, j, a, e);
           const bool part = is_v && (a > 0 || e < 128);
           // A tile to be zeroed waits until the next load is out, or has no slot yet.
-          if (fix >= 0 && (part || (round && !__all_sync(0xffffffffu, mbar_test(&empty[slot], turn ^ 1)))))
-            if (!(ok = zero_rows())) break;
-          if (round && !(ok = wait_all(&empty[slot], turn ^ 1))) break;
-          if (!skip) load_tile(it, j, pg, ring + slot * C::TILE, part ? &v_raw[slot] : &full[slot]);
-          skip = false;
-          if (fix >= 0 && !(ok = zero_rows())) break;
+          bool loaded = false;
+#pragma unroll 1
+          for (;;) {
+            if (!loaded && !(fix >= 0 && (part || (round && !__all_sync(0xffffffffu, mbar_test(&empty[slot], turn ^ 1)))))) {
+              if (round && !(ok = wait_all(&empty[slot], turn ^ 1))) break;
+              if (!skip) load_tile(it, j, pg, ring + slot * C::TILE, part ? &v_raw[slot] : &full[slot]);
+              skip = false;
+              loaded = true;
+            }
+            if (fix >= 0 && !(ok = zero_rows())) break;
+            if (loaded) break;
+          }
+          if (!ok) break;
           if (part) fix = slot, fix_a = a, fix_e = e;
           if (++slot == slots) slot = 0, turn ^= 1, round = true;
           if (QT == 2 && !is_v && jj == 0 && it.hi[1] > 0) ok = load_q(1);
@@ -793,9 +807,11 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // Every copy that was issued lands before the CTA leaves, on a timeout too.
         volatile int no_abort = 0;
         WaitCtl dw{p.status, &no_abort, 100000000ull};
+#pragma unroll 1
         for (int i = max(0, qc - C::QS); i < qc; ++i)
           mbar_wait_far(&q_full[i % C::QS], (i / C::QS) & 1, dw, kQSiteDrain);
         if (fix >= 0) mbar_wait_far(&v_raw[fix], raw_par >> fix & 1, dw, kQSiteDrain);
+#pragma unroll 1
         for (int i = 0; i < slots; ++i) {
           // Slots before `slot` were last loaded in this turn, the others in the one before.
           const bool now = i < slot;
@@ -824,15 +840,15 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       uint32_t par = 0;  // parity of the turn around the ring
       if (warp == 9) {
         const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
-        ShareWalk<QT> walk;
+        ShareWalk<QT, kItemUnits> walk;
         walk.start(p, held, lane);
         SeqItem it{};
-        bool have = walk.next(p, lane, it);  // `it` is still to be handed out
-        int out = 0, in = 0, c = 0;          // items handed out, and begun here; steps issued
-        bool ended = false;
+        int out = 0, in = 0, c = 0;  // items handed out, and begun here; steps issued
+        bool have = false, next = true, ended = false;  // `it` is to be handed out; is to be found
         for (;;) {
           // Items go out as ring slots come free; waited for only when there is none to begin.
           while (ok && !ended) {
+            if (next) have = walk.next(p, lane, it), next = false;
             const int s = out % NI;
             if (out >= NI) {
               const uint32_t turn = ((out / NI) - 1) & 1;
@@ -846,7 +862,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             __syncwarp();
             ++out;
-            if (have) have = walk.next(p, lane, it);
+            next = have;
           }
           if (!ok) break;
           // The next item is begun.  (Its slot was written by this warp.)
@@ -1202,26 +1218,28 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (ok && mine) ok = product(pc - 1);
       float* ex = reinterpret_cast<float*>(myP);  // [4][2][N] sums, [N] maxima (P is not read any more)
       if (steps > 0) {
-        // Lane n < N ends up with the warp's sums of row n.
-        float sl = 0.f, sr2 = 0.f, mm = -INFINITY;
+        // Each exchange halves the rows that a lane sums: 31 instead of 160 for all, and a
+        // quarter of the code.  Lane 2 n (and 2 n + 1) ends up with the warp's sums of row n.
+        static_assert(N == 16, "four halvings");
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (n < rows) {
-            float a = l[n], q = lr[n];
+        for (int h = N / 2; h >= 1; h >>= 1) {
+          const bool up = lane & (2 * h);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              a += __shfl_xor_sync(0xffffffffu, a, o);
-              q += __shfl_xor_sync(0xffffffffu, q, o);
-            }
-            if (lane == n) sl = a, sr2 = q, mm = m[n];
+          for (int n = 0; n < h; ++n) {
+            const float a = up ? l[n] : l[n + h], q = up ? lr[n] : lr[n + h];
+            l[n] = (up ? l[n + h] : l[n]) + __shfl_xor_sync(0xffffffffu, a, 2 * h);
+            lr[n] = (up ? lr[n + h] : lr[n]) + __shfl_xor_sync(0xffffffffu, q, 2 * h);
+            m[n] = up ? m[n + h] : m[n];
           }
         }
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+        lr[0] += __shfl_xor_sync(0xffffffffu, lr[0], 1);
         // (P's buffer is free once this warpgroup's last product is done, for all its warps.)
         ok = named_bar_and(wg_bar, 128, ok);
-        if (ok && lane < N) {
-          ex[(wq * 2) * N + lane] = sl;
-          ex[(wq * 2 + 1) * N + lane] = sr2;
-          if (wq == 0) ex[8 * N + lane] = mm;
+        if (ok && !(lane & 1)) {
+          ex[(wq * 2) * N + (lane >> 1)] = l[0];
+          ex[(wq * 2 + 1) * N + (lane >> 1)] = lr[0];
+          if (wq == 0) ex[8 * N + (lane >> 1)] = m[0];
         }
         tc_fence_before();
       }
@@ -1232,21 +1250,19 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const float* e1 = reinterpret_cast<const float*>(sP + C::PB * C::PBUF);
       const int n0 = w * H2;
       if (n0 < rows) {
-        uint32_t o0[H2], o1[H2];
-        if (steps > 0) {
-          tmem_ld8(tmem_addr(tbase, lb, C::O_COL(0) + n0), o0);
-          tmem_ld8(tmem_addr(tbase, lb, C::O_COL(1) + n0), o1);
-          tmem_wait_ld();
-          reg_fence(o0);
-          reg_fence(o1);
-        }
         // Which warpgroups have a part: with one step only the one whose turn it was.
         const bool has0 = steps > 1 || (steps == 1 && (c & 1) == 0), has1 = steps > 1 || (steps == 1 && (c & 1) == 1);
         int tok = n0 / G, g = n0 - tok * G;
-#pragma unroll
-        for (int i = 0; i < H2; ++i) {
-          const int n = n0 + i;
-          if (n < rows) {
+        // Row by row: unrolled, this was 24 KB of code, run cold at every item's end.
+#pragma unroll 1
+        for (int n = n0; n < min(rows, n0 + H2); ++n) {
+          {
+            uint32_t o0[1], o1[1];
+            tmem_ld1(tmem_addr(tbase, lb, C::O_COL(0) + n), o0);
+            tmem_ld1(tmem_addr(tbase, lb, C::O_COL(1) + n), o1);
+            tmem_wait_ld();
+            reg_fence(o0);
+            reg_fence(o1);
             const float m0 = has0 ? e0[8 * N + n] : -INFINITY, m1 = has1 ? e1[8 * N + n] : -INFINITY;
             const float M = fmaxf(m0, m1);
             const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
@@ -1258,8 +1274,8 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             const float inv = (L > 0.f && R > 0.f) ? 1.0f / R : 0.f;
             const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
-            float y = a0 > 0.f ? a0 * __uint_as_float(o0[i]) : 0.f;
-            if (a1 > 0.f) y += a1 * __uint_as_float(o1[i]);
+            float y = a0 > 0.f ? a0 * __uint_as_float(o0[0]) : 0.f;
+            if (a1 > 0.f) y += a1 * __uint_as_float(o1[0]);
             y *= inv;
             const int row = row0 + tok, head = kvh * G + g;
             if (part < 0) {
@@ -1339,8 +1355,14 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const int hi_lim = klast - kc0 + 1, lo_lim = kfirst - kc0;
           if (__any_sync(0xffffffffu, hi_lim < 128 || lo_lim > 0)) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= hi_lim || i < lo_lim) sr[i] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 4; ++c) {
+              // Bits lo .. hi - 1 of 32 keys: two comparisons a key were 5 KB more of code.
+              const int hi = min(max(hi_lim - 32 * c, 0), 32), lo = min(max(lo_lim - 32 * c, 0), 32);
+              const uint32_t keep = static_cast<uint32_t>(((1ull << hi) - 1) & ~((1ull << lo) - 1));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(keep & (1u << i))) sr[32 * c + i] = __float_as_uint(-INFINITY);
+            }
           }
           float mx[8];
 #pragma unroll
@@ -1451,7 +1473,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int row = it.row0 + tok, head = it.kvh * G + g_r;
         uint16_t* orow = p.O + row * p.o_row + head * p.o_head;
         const size_t prow = (static_cast<size_t>(max(part, 0)) * QT + t) * 128 + r_loc;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
           if (steps > 0) {

@@ -639,10 +639,9 @@ def paged_tables(context_lens, new_lens, free_blocks, block_table, T: int, block
     """Tables of a step of at most T new tokens: (block_table, updated in place,
     cu_seqlens [B+1], seq_lens [B], positions [T], slots [T], used [1])."""
     B = _dims("block_table", block_table, 2)[0]
+    empty = block_table.new_empty
     with _home(block_table, stream):
-        # one allocation for the five: their time is most of the call's
-        cu, lens, positions, slots, used = block_table.new_empty(2 * B + 2 * T + 2).split(
-            (B + 1, B, T, T, 1))
+        cu, lens, positions, slots, used = empty(B + 1), empty(B), empty(T), empty(T), empty(1)
     rc = fa2_paged_tables(context_lens, new_lens, free_blocks, block_table, cu, lens, positions,
                           slots, used, block_size, stream)
     if rc != FA2_OK:

@@ -388,6 +388,8 @@ size_t fa2_fwd_paged_workspace_size(int B, int T, int H, int Hkv, int d, int sm_
  *                 fa2_get_device_status.
  *   workspace   : at least fa2_fwd_paged_workspace_size() bytes, 256-byte aligned, not
  *                 shared with a call that may run at the same time
+ * (B + T * (H / Hkv) / 256) * (max_blocks * block_size / 128 + 6) * Hkv has to stay below
+ * about 2^30 (FA2_ERR_INVALID_ARG; for few tokens to a request, 128 or 16 in place of 256).
  * Cache positions from seq_lens[b] on may hold anything, NaN included.  d a multiple of
  * 8 up to 256.  Results are bitwise repeatable on one GPU.
  */

@@ -33,6 +33,9 @@ __device__ __forceinline__ int blocks_for(int n, int bs) { return n > 0 ? (n - 1
 // writes the table rows of every gridDim-th request and the slots of its own stretch
 // of tokens.  No CTA waits for another: a slot whose block is new in this step is taken
 // from the free list again rather than from the table entry that another CTA writes.
+// A step of 64 single tokens takes 5 us, 500 requests that bring 0.67 M tokens 15 us (B200): the
+// chain of loads, the scan and each token's search, not the 5.7 MB; a call from Python takes 17
+// us, the host's time.
 // Sums past 2^31 give unspecified tables, but every index below is checked or clamped, so
 // that none reads or writes outside them.
 __global__ void __launch_bounds__(kTablesThreads)

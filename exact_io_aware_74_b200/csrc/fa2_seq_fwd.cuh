@@ -245,6 +245,7 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
                                            UnitAt& r) {
   int total = 0, rem = 0;
   int units = 1;  // of one head of the sequence found
+  r.b = -1;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -282,8 +283,10 @@ __device__ __forceinline__ bool find_share(const SeqParams& p, int grid, int c, 
       __syncwarp();
     }
   }
+  if (r.b < 0) return false;  // (offsets that fall can hold more rows than T, and the sums wrap)
   r.s = seq_len<true>(p, r.b);
   r.kvh = static_cast<unsigned int>(rem) / static_cast<unsigned int>(units);
+  if (static_cast<unsigned int>(r.kvh) >= static_cast<unsigned int>(p.Hkv)) return false;  // (likewise)
   int at = rem - r.kvh * units;
   const int R = QT * p.tpt, nb = blocks_of(r.s.n, R);
   r.blk = 0;
@@ -360,7 +363,11 @@ struct ShareWalk {
         u.blk = 0;
         if (++u.kvh >= p.Hkv) {
           u.kvh = 0;
-          do u.s = seq_len<true>(p, ++u.b); while (u.s.n == 0 && u.b + 1 < p.B);  // units are left
+          do {
+            if (++u.b >= p.B) break;  // (likewise: units are left otherwise)
+            u.s = seq_len<true>(p, u.b);
+          } while (u.s.n == 0);
+          if (u.b >= p.B) x = xe;
         }
       }
     }

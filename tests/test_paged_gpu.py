@@ -206,6 +206,26 @@ def test_blocks_outside_the_cache_are_reported():
     s.check()
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 300, 7]])
+def test_bad_offsets_stay_inside_the_tensors(new):
+    """Offsets that fall, repeat or leave the tensors, and lengths of any sign: nothing outside the
+    outputs is touched (the results are unspecified)."""
+    s = Step([200, 0, 500], new, 4, 2, 64, 16, "bf16", seed=32)
+    T = s.q.shape[0]
+    s.table.clamp_(0)  # entries that a wrong length may reach
+    buf = torch.full((T + 2, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4 * T + 2,), 7.0, device="cuda")
+    ws = torch.empty(fa2.fa2_fwd_paged_workspace_size(3, T, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    top = 2 ** 31 - 1
+    for at, lens in (([0, T, 0, T], [200, 500, 90]), ([-5, 1, top, 2], [1, top, 30]), ([T, 0, T, -top - 1], [60] * 3),
+                     ([0, T, T, T], [-7, -top - 1, top])):
+        assert fa2.fa2_fwd_paged(s.q, s.k_cache, s.v_cache, buf[1:T + 1], lse[1:-1].view(4, T), s.table, ints(at),
+                                 ints(lens), ws, s.scale, True) == fa2.FA2_OK
+        ok()
+        assert (buf[0] == 7).all() and (buf[T + 1] == 7).all() and lse[0] == 7 and lse[-1] == 7
+    s.check()
+
+
 def test_repeatable():
     s = Step([5000, 129, 0, 2000], [1, 1, 1, 1], 16, 4, 128, 16, "bf16", seed=11)
     o, lse = s.run()

@@ -1472,9 +1472,11 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (!ok) break;
         tc_fence_after();
       }
-      // A row that sees no key: O = 0, LSE = -inf.
-      const float inv_l = (l > 0.f && lr > 0.f) ? 1.0f / lr : 0.f;
-      const float lse = (l > 0.f) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      // A row that sees no key: O = 0, LSE = -inf.  Its sum is exactly zero (any other has weights of
+      // about one and more); the sum of a row that sees a NaN or a score of +inf is NaN, and so are
+      // its O and LSE.
+      const float inv_l = l == 0.f ? 0.f : 1.0f / lr;
+      const float lse = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
       const int part = PAGED ? it.part : -1;  // packed items are never cut
       if (live) {
         const int row = it.row0 + tok, head = it.kvh * G + g_r;

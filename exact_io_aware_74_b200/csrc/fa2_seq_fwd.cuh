@@ -1506,7 +1506,7 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                   *reinterpret_cast<uint4*>(orow + c * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-          } else if (row_ok && l > 0.f) {
+          } else if (row_ok && l != 0.f) {
             float4* dst = reinterpret_cast<float4*>(p.O_part + prow * D + c * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -1562,39 +1562,38 @@ __global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p) {
     const auto slot = [&](int s) {  // row of part s: the first is its share's second slot
       return (static_cast<size_t>(2 * (c + s) + (s == 0 ? 1 : 0)) * QT) * 128 + r;
     };
+    // The maximum passes over a NaN; the weights then bring it into the sums.
     float M = -INFINITY;
     for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.LSE_part[slot(s)]);
     M = warp_max(M);
     float acc[PER] = {}, wsum = 0.f;
-    if (M != -INFINITY) {
-      for (int s0 = 0; s0 < parts; s0 += U) {
-        float L[U], v[U][PER];
+    for (int s0 = 0; s0 < parts; s0 += U) {
+      float L[U], v[U][PER];
 #pragma unroll
-        for (int k = 0; k < U; ++k) L[k] = s0 + k < parts ? p.LSE_part[slot(s0 + k)] : -INFINITY;
+      for (int k = 0; k < U; ++k) L[k] = s0 + k < parts ? p.LSE_part[slot(s0 + k)] : -INFINITY;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          // A part of whose keys the row sees none was not written.
-          if (L[k] != -INFINITY) {
-            const float* src = p.O_part + slot(s0 + k) * D + lane * PER;
+      for (int k = 0; k < U; ++k) {
+        // A part of whose keys the row sees none was not written.
+        if (L[k] != -INFINITY) {
+          const float* src = p.O_part + slot(s0 + k) * D + lane * PER;
 #pragma unroll
-            for (int e = 0; e < PER; e += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(src + e);
-              v[k][e] = f.x;
-              v[k][e + 1] = f.y;
-            }
+          for (int e = 0; e < PER; e += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(src + e);
+            v[k][e] = f.x;
+            v[k][e + 1] = f.y;
           }
         }
+      }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          if (L[k] == -INFINITY) continue;
-          const float w = exp2f((L[k] - M) * 1.4426950408889634f);
-          wsum += w;
+      for (int k = 0; k < U; ++k) {
+        if (L[k] == -INFINITY) continue;
+        const float w = exp2f((L[k] - M) * 1.4426950408889634f);
+        wsum += w;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
-        }
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
       }
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;  // 0: no part with a key
     const int row = at.x + tok, head = at.z * p.G + g;
     uint16_t* dst = p.O + row * p.o_row + head * p.o_head + lane * PER;
 #pragma unroll
@@ -1602,7 +1601,7 @@ __global__ void __launch_bounds__(256) fa2_seq_merge_kernel(const SeqParams p) {
       if (lane * PER + e < p.d)
         *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0)
-      p.LSE[static_cast<size_t>(head) * p.T + row] = wsum > 0.f ? M + logf(wsum) : -INFINITY;
+      p.LSE[static_cast<size_t>(head) * p.T + row] = wsum == 0.f ? -INFINITY : M + logf(wsum);
   }
 }
 

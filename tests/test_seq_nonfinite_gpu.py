@@ -1,4 +1,4 @@
-"""NaN and infinities among the values that rows see, in the packed forward.
+"""NaN and infinities among the values that rows see, in the packed and paged forward.
 
 A row whose scores hold a NaN or a +inf has no finite softmax: the 64-bit reference is not
 finite there, and neither may the result be, in O (NaN) and in LSE (NaN or +inf, never the -inf
@@ -10,7 +10,8 @@ import torch
 
 from exact_io_aware_74_b200 import fa2
 from packed_ref import assert_within, packed_forward
-from test_varlen_gpu import make, ok
+from test_paged_gpu import Step, ok
+from test_varlen_gpu import make
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,37 @@ def test_packed(lens, d, where, bad):
     o, lse = fa2.forward_varlen(q, k, v, cu, d ** -0.5, True)
     ok()
     compare(o, lse, *packed_forward(q, k, v, lens, d ** -0.5, True))
+
+
+# ------------------------------------------------------------------ paged
+
+def check_paged(context, new, H, Hk, d, where, bad, window=0, dtype="bf16"):
+    """Request 1 holds the bad value: in its last query, or in a key that it sees."""
+    s = Step(context, new, H, Hk, d, 16, dtype, seed=3)
+    g = H // Hk
+    row = sum(new[:2]) - 1
+    if where == "query":
+        s.q[row, g, 3] = bad
+    else:
+        s.q[..., 3] = s.q[..., 3].abs() + 0.5
+        key = s.total[1] - 2 if where == "late key" else 1
+        s.caches[1][0][key, 1, 3] = bad
+        s.k_cache[int(s.table[1, key // 16]), 1, key % 16, 3] = bad
+    for causal in (True, False):
+        o, lse = s.run(causal, window if causal else 0)
+        compare(o, lse, *packed_forward(s.q, None, None, s.new, s.scale, causal, window if causal else 0, s.caches))
+
+
+# Short caches: every request's key tiles lie in one share.  Long ones: they are cut.
+SHORT, LONG = [60, 100, 5], [700, 4000, 90]
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("where", ["query", "key", "late key"])
+@pytest.mark.parametrize("context,new,d", [
+    ([0, 3, 5], [20, 24, 22], 64), (LONG, [20, 24, 22], 128), (SHORT, [1, 1, 1], 256), (LONG, [1, 1, 1], 256),
+    ([0, 3, 0], [50, 60, 70], 64), (LONG, [300, 200, 100], 64), (LONG, [300, 200, 100], 128)],
+    ids=["one-tile", "one-tile-cut", "one-tile-256", "one-tile-256-cut", "two-tiles", "two-tiles-cut-64",
+         "two-tiles-cut-128"])
+def test_paged_tiles(context, new, d, where, bad):
+    check_paged(context, new, 8, 2, d, where, bad)

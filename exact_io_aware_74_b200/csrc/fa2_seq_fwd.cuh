@@ -1270,20 +1270,28 @@ fa2_seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tmem_wait_ld();
             reg_fence(o0);
             reg_fence(o1);
-            const float m0 = has0 ? e0[8 * N + n] : -INFINITY, m1 = has1 ? e1[8 * N + n] : -INFINITY;
-            const float M = fmaxf(m0, m1);
-            const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
-            float L = 0.f, R = 0.f;
+            // A part counts if its sum is not exactly zero, which means a row that sees none of its
+            // keys.  The maxima pass over a NaN (and are -inf where every score is one); the sums
+            // carry it, and the weights of +inf, NaN too, through to O and LSE.
+            float l0 = 0.f, r0 = 0.f, l1 = 0.f, r1 = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              if (a0 > 0.f) L += a0 * e0[q * 2 * N + n], R += a0 * e0[(q * 2 + 1) * N + n];
-              if (a1 > 0.f) L += a1 * e1[q * 2 * N + n], R += a1 * e1[(q * 2 + 1) * N + n];
+              if (has0) l0 += e0[q * 2 * N + n], r0 += e0[(q * 2 + 1) * N + n];
+              if (has1) l1 += e1[q * 2 * N + n], r1 += e1[(q * 2 + 1) * N + n];
             }
-            const float inv = (L > 0.f && R > 0.f) ? 1.0f / R : 0.f;
-            const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
-            float y = a0 > 0.f ? a0 * __uint_as_float(o0[0]) : 0.f;
-            if (a1 > 0.f) y += a1 * __uint_as_float(o1[0]);
-            y *= inv;
+            const float m0 = l0 != 0.f ? e0[8 * N + n] : -INFINITY, m1 = l1 != 0.f ? e1[8 * N + n] : -INFINITY;
+            const float M = fmaxf(m0, m1);
+            float L = 0.f, R = 0.f, y = 0.f;
+            if (l0 != 0.f) {
+              const float a = ex2_approx(m0 - M);
+              L = a * l0, R = a * r0, y = a * __uint_as_float(o0[0]);
+            }
+            if (l1 != 0.f) {
+              const float a = ex2_approx(m1 - M);
+              L += a * l1, R += a * r1, y += a * __uint_as_float(o1[0]);
+            }
+            const float lse = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+            y *= L == 0.f ? 0.f : 1.0f / R;
             const int row = row0 + tok, head = kvh * G + g;
             if (part < 0) {
               if (r < p.d)

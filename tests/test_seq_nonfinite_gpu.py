@@ -70,8 +70,9 @@ def check_paged(context, new, H, Hk, d, where, bad, window=0, dtype="bf16"):
         compare(o, lse, *packed_forward(s.q, None, None, s.new, s.scale, causal, window if causal else 0, s.caches))
 
 
-# Short caches: every request's key tiles lie in one share.  Long ones: they are cut.
-SHORT, LONG = [60, 100, 5], [700, 4000, 90]
+# Short caches: every request's key tiles lie in one share.  Long ones: they are cut, into shares
+# of two units where there are few requests, into longer ones where there are many.
+SHORT, LONG, MANY = [60, 100, 5], [700, 4000, 90], [3000] * 40
 
 
 @pytest.mark.parametrize("bad", BAD)
@@ -83,3 +84,23 @@ SHORT, LONG = [60, 100, 5], [700, 4000, 90]
          "two-tiles-cut-128"])
 def test_paged_tiles(context, new, d, where, bad):
     check_paged(context, new, 8, 2, d, where, bad)
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("where", ["query", "key", "late key"])
+@pytest.mark.parametrize("context", [SHORT, LONG, MANY], ids=["whole", "cut", "cut-seldom"])
+@pytest.mark.parametrize("H,Hk,d,dtype", [(8, 2, 64, "bf16"), (8, 2, 128, "fp16"), (32, 2, 128, "bf16")])
+def test_paged_few_rows(context, H, Hk, d, dtype, where, bad):
+    check_paged(context, [1] * len(context), H, Hk, d, where, bad, dtype=dtype)
+    if context is not SHORT and where != "key":
+        check_paged(context, [1] * len(context), H, Hk, d, where, bad, window=300, dtype=dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_queries_that_are_all_nan(d):
+    """Every score of every row: no weight has a finite maximum to be measured from."""
+    for context, new in ((SHORT, [1, 1, 1]), (LONG, [1, 1, 1]), (LONG, [30, 20, 22]), (LONG, [300, 200, 100])):
+        s = Step(context, new, 8, 2, d, 16, "bf16", seed=4)
+        s.q.fill_(float("nan"))
+        o, lse = s.run()
+        assert torch.isnan(o.float()).all() and torch.isnan(lse).all()

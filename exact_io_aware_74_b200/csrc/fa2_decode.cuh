@@ -51,7 +51,7 @@ fa2_decode_combine_kernel(const float* __restrict__ O_part, const float* __restr
   if (row >= rows) return;  // whole warp leaves together
   constexpr float kLog2e = 1.4426950408889634f;
 
-  float M = -INFINITY;
+  float M = -INFINITY;  // passes over a NaN; the weights then bring it into the sums
   for (int s = lane; s < n_split; s += 32) M = fmaxf(M, LSE_part[s * rows + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -60,45 +60,43 @@ fa2_decode_combine_kernel(const float* __restrict__ O_part, const float* __restr
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
   float wsum = 0.f;
-  if (M != -INFINITY) {
-    for (int s0 = 0; s0 < n_split; s0 += 32) {
-      // Lane c weighs split s0 + c; the weights are then broadcast, and U
-      // partial rows are loaded before any is used.  A split the row sees no
-      // key of has weight 0 and its (unwritten) partial row is not read.
-      const int s = s0 + lane;
-      const float L = (s < n_split) ? LSE_part[s * rows + row] : -INFINITY;
-      const float w = (L == -INFINITY) ? 0.f : exp2f((L - M) * kLog2e);
-      wsum += w;
-      const int cnt = min(32, n_split - s0);
-      for (int c0 = 0; c0 < cnt; c0 += U) {
-        float wc[U], v[U][PER];
+  for (int s0 = 0; s0 < n_split; s0 += 32) {
+    // Lane c weighs split s0 + c; the weights are then broadcast, and U
+    // partial rows are loaded before any is used.  A split the row sees no
+    // key of has weight 0 and its (unwritten) partial row is not read.
+    const int s = s0 + lane;
+    const float L = (s < n_split) ? LSE_part[s * rows + row] : -INFINITY;
+    const float w = (L == -INFINITY) ? 0.f : exp2f((L - M) * kLog2e);
+    wsum += w;
+    const int cnt = min(32, n_split - s0);
+    for (int c0 = 0; c0 < cnt; c0 += U) {
+      float wc[U], v[U][PER];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int c = c0 + u;
-          wc[u] = __shfl_sync(0xffffffffu, w, c & 31);
-          if (c >= cnt) wc[u] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u;
+        wc[u] = __shfl_sync(0xffffffffu, w, c & 31);
+        if (c >= cnt) wc[u] = 0.f;
 #pragma unroll
-          for (int i = 0; i < PER; ++i) v[u][i] = 0.f;
-          if (wc[u] != 0.f) {  // warp-uniform
-            const float* src = O_part + ((s0 + c) * rows + row) * D + lane * PER;
+        for (int i = 0; i < PER; ++i) v[u][i] = 0.f;
+        if (wc[u] != 0.f) {  // warp-uniform
+          const float* src = O_part + ((s0 + c) * rows + row) * D + lane * PER;
 #pragma unroll
-            for (int i = 0; i < PER / 2; ++i) {  // 8-byte aligned pairs
-              const float2 t = reinterpret_cast<const float2*>(src)[i];
-              v[u][2 * i] = t.x;
-              v[u][2 * i + 1] = t.y;
-            }
+          for (int i = 0; i < PER / 2; ++i) {  // 8-byte aligned pairs
+            const float2 t = reinterpret_cast<const float2*>(src)[i];
+            v[u][2 * i] = t.x;
+            v[u][2 * i + 1] = t.y;
           }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int i = 0; i < PER; ++i) acc[i] = fmaf(wc[u], v[u][i], acc[i]);
       }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(wc[u], v[u][i], acc[i]);
+    }
   }
-  const float inv = (wsum > 0.f) ? 1.f / wsum : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;  // 0: the row sees no key
   uint32_t packed[PER / 2];
 #pragma unroll
   for (int i = 0; i < PER / 2; ++i) packed[i] = pack2<BF16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
@@ -106,7 +104,7 @@ fa2_decode_combine_kernel(const float* __restrict__ O_part, const float* __restr
 #pragma unroll
   for (int i = 0; i < PER / 2; ++i)
     if (lane * PER + 2 * i < d) dst[i] = packed[i];  // d is even: whole pairs
-  if (lane == 0) LSE[row] = (wsum > 0.f) ? M + logf(wsum) : -INFINITY;
+  if (lane == 0) LSE[row] = wsum == 0.f ? -INFINITY : M + logf(wsum);
 }
 
 }  // namespace fa2

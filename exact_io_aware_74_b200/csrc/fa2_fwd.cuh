@@ -749,10 +749,11 @@ fa2_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (my_nkv - 1) & 1, wc, kSiteSoftOEnd));
     if (ok && live) {
       tc_fence_after();
-      // A row can see no key of a split (l = 0): it contributes nothing.
+      // A row can see no key of a split (l = 0 exactly): it contributes nothing.  The sum
+      // of a row that sees a NaN or a score of +inf is NaN, and so are its O and LSE.
       // (8-bit inputs: the scale of V is applied here, once per output element.)
-      const float inv_l = (l > 0.f && lr > 0.f) ? (F8 ? p.o_scale : 1.0f) / lr : 0.f;
-      const float lse = (l > 0.f) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      const float inv_l = l == 0.f ? 0.f : (F8 ? p.o_scale : 1.0f) / lr;
+      const float lse = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
       const size_t orow_idx = static_cast<size_t>(bh) * Nq + row;
       if (!partial) {
         const int d = p.d;
@@ -786,7 +787,7 @@ fa2_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           tmem_ld32(tmem_addr(tbase, lane_base, o_col + 32 * c), r);
           tmem_wait_ld();
           reg_fence(r);
-          if (row < Nq && l > 0.f) {
+          if (row < Nq && l != 0.f) {
             float4* dst = reinterpret_cast<float4*>(orow + c * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -353,7 +353,10 @@ def _home(t, stream):
     if stream is None:
         return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        # Handle 0 is the default stream, and 1 (cudaStreamLegacy) another name of it.  torch takes
+        # 0 for no handle and makes a stream of its own, and does not know 1.
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream) > 1 else \
+            torch.cuda.default_stream(t.device)
     return torch.cuda.stream(stream)
 
 

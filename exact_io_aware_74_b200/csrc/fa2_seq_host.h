@@ -17,10 +17,12 @@ struct SeqMaps {
 // Kernel head dim (tile width) for head dim d.
 inline int seq_tile_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
 
-// qt: query tiles to an item (2 only up to d = 128); grid: CTAs.  Both return an fa2_status.
+// qt: query tiles to an item, 1 or 2 (2 only up to d = 128).  form: 1 or 2 query tiles, or 16: items
+// of at most 16 rows with the products' operands swapped (d <= 128).  grid: CTAs.  Both return an
+// fa2_status.
 int launch_seq_packed(int d, bool bf16, int qt, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
                       cudaStream_t s);
-int launch_seq_paged(int d, bool bf16, int qt, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
+int launch_seq_paged(int d, bool bf16, int form, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
                      cudaStream_t s);
 
 struct SeqBwdParams;

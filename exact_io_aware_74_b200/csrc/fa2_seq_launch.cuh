@@ -46,17 +46,17 @@ int launch_seq(const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid,
   return FA2_OK;
 }
 
-// qt: 2 or 1 query tiles of 128 rows, or (paged, d <= 128) 16: few rows.
+// form: 2 or 1 query tiles of 128 rows, or (paged, d <= 128) 16: few rows.
 template <bool PAGED, bool BF16>
-int launch_seq_any(int d, int qt, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid, cudaStream_t s) {
+int launch_seq_any(int d, int form, const SeqMaps& m, const SeqParams& p, int dev, unsigned int grid, cudaStream_t s) {
   if constexpr (PAGED) {
-    if (qt == 16) return d <= 64 ? launch_seq<64, BF16, 1, true, 16>(m, p, dev, grid, s) : launch_seq<128, BF16, 1, true, 16>(m, p, dev, grid, s);
+    if (form == 16) return d <= 64 ? launch_seq<64, BF16, 1, true, 16>(m, p, dev, grid, s) : launch_seq<128, BF16, 1, true, 16>(m, p, dev, grid, s);
   }
   switch (seq_tile_dim(d)) {
     case 64:
-      return qt == 2 ? launch_seq<64, BF16, 2, PAGED>(m, p, dev, grid, s) : launch_seq<64, BF16, 1, PAGED>(m, p, dev, grid, s);
+      return form == 2 ? launch_seq<64, BF16, 2, PAGED>(m, p, dev, grid, s) : launch_seq<64, BF16, 1, PAGED>(m, p, dev, grid, s);
     case 128:
-      return qt == 2 ? launch_seq<128, BF16, 2, PAGED>(m, p, dev, grid, s) : launch_seq<128, BF16, 1, PAGED>(m, p, dev, grid, s);
+      return form == 2 ? launch_seq<128, BF16, 2, PAGED>(m, p, dev, grid, s) : launch_seq<128, BF16, 1, PAGED>(m, p, dev, grid, s);
     case 192: return launch_seq<192, BF16, 1, PAGED>(m, p, dev, grid, s);
     default: return launch_seq<256, BF16, 1, PAGED>(m, p, dev, grid, s);
   }

@@ -55,12 +55,14 @@ bool cache_ok(const fa2_cache* x, int blocks, int heads, int rows, int d) {
 int partial_blocks(int B, int T, int held) { return B > held ? B : std::min(B, T); }
 
 // Key/value heads to a group of the item order: as many equal groups as leave each `waves`
-// waves of items.  Fewer leave SMs without work where a group's longest items start last,
-// more let the heads' rows fall out of L2.  Measured on B200 (heads to a group): backward of
-// 14k tokens, d = 128, 890 items of very different length: 1: 1762, 3: 1727, 4: 1620, 8: 1570
-// us, of 8 x 4096 tokens, 4200 items: 3: 1900, 5: 2012 us; forward of 15k tokens, d = 64,
-// 1050 items: 1: 177, 3: 162, 8: 142 us, of 22k tokens, d = 128, 2800 items: 1: 1258, 4: 1214,
-// 8: 1226 us.
+// waves of items.  Fewer heads leave SMs without work where a group's longest items start last,
+// more let the heads' rows fall out of L2.  Measured on B200 (heads to a group, replayed graphs;
+// the calls of 1 ms and more vary by 5 % with the power limit): backward of 14k tokens, d = 128, 920
+// items of very different length: 1: 1748, 2: 1738, 3: 1761, 4: 1649, 8 (the rule): 1560 to 1630 us; of
+// 4k tokens, d = 64, 4 heads: 1: 111, 2: 100, 4 (the rule): 82 us; of 8 x 4096 tokens, d = 128, 16
+// heads, 4200 items: 1: 1989, 3 (the rule): 2011 to 2059, 5: 2140, 8: 2183, 16: 2466 us.  Forward of 15k
+// tokens, d = 64, 1050 items: 1: 158, 2: 143, 3: 147, 4: 134, 8 (the rule): 128 us; of 22k tokens,
+// d = 128, 2800 items: 1: 1209, 2: 1164, 3 (the rule): 1185, 4: 1211, 8: 1213 us.
 int head_group(long long items, int waves, int Hkv, int n_sm) {
   const long long groups = std::min<long long>(Hkv, std::max(1ll, items / (static_cast<long long>(waves) * n_sm)));
   return static_cast<int>((Hkv + groups - 1) / groups);
@@ -116,10 +118,17 @@ fa2::SeqParams seq_params(const fa2_packed* O, float* LSE, const int* cu, unsign
 
 // Form of a paged call's items, by the rows that the requests bring on average: two query
 // tiles of 128 rows (prompts, chunks), one, or 16 rows with the products' operands swapped
-// (decode steps; d <= 128).  Every form is right for every batch.  Measured on B200, caches of
-// 6k tokens, 16 rows -> one tile: d = 64: 1 row 171 -> 237 us, 4 rows 184 -> 237, 16 rows 179
-// -> 196; d = 128: 268 -> 301, 270 -> 302, 233 -> 251 us.  (The swapped form with 32 rows spilled
-// and took 660 us, one tile 203: it was dropped.)
+// (decode steps; d <= 128).  Every form is right for every batch.  Measured on B200 (replayed graphs,
+// single tokens, 8 key/value heads, blocks of 16), 16 rows against one tile:
+//   64 requests of up to 6000 tokens, 1, 4, 16 heads to a group: d = 64: 121, 123, 139 us against 147,
+//     148, 149; d = 128: 166, 170, 174 against 163, 165, 171
+//   4 heads to a group: 64 requests of up to 8192 tokens: d = 64: 170 to 183 against 193 to 197, d = 128:
+//     225 against 218; of up to 700: d = 64: 41.2 against 39.5, d = 128: 47.3 against 44.1; 4 of up to
+//     32768: d = 64: 56 against 62, d = 128: 73.5 against 71.5; 4 of up to 700: 14.0 against 13.3, 14.4
+//     against 13.6
+// So 16 rows gain 7 to 18 % on long caches of 64-column heads and cost 1 to 7 % elsewhere, where the
+// rule, which looks at the rows alone, takes them all the same.  (The swapped form with 32 rows spilled
+// and took 660 us where one tile took 203: it was dropped.)
 int paged_form(int B, int T, int G, int d) {
   if (d > 128) return 1;
   const long long rows = static_cast<long long>(T) * G, b = B;

@@ -30,6 +30,11 @@
  *     returns (work is enqueued on ``stream``).
  *   - ``causal`` = 1 lets query row i see keys 0..i; 0 lets it see all keys.
  *   - LSE_i = ln sum_j exp(S_ij) over the keys row i sees, S = scale * Q K^T.
+ *   - A row that sees a NaN or a score of +inf gets an O of NaN and an LSE that is
+ *     NaN, however its keys are split; a row whose scores are all -inf counts as one
+ *     that sees no key (O = 0, LSE = -inf).  A NaN or an infinity in a row of V can
+ *     also reach the rows of its sequence that do not see that key, and in K, V, Q
+ *     or dO every gradient of its sequence: a weight of zero does not hide it.
  *   - The return value reports argument validation and launch only; the kernels
  *     run asynchronously.  Failures inside a kernel (a bounded wait that ran out)
  *     are reported by fa2_get_device_status().
@@ -325,7 +330,7 @@ typedef struct {
  *   Q, O       : [T] x H heads of d columns (in, out)
  *   K, V       : [T] x Hkv heads of d columns (in)
  *   LSE        : out, [H][T] float
- *   cu_seqlens : in, [B + 1] int
+ *   cu_seqlens : in, [B + 1] int, B >= 1
  *   T          : >= 0 (0 launches nothing); d a multiple of 8 up to 256
  *   window     : 0, or >= 1 with causal = 1
  * What lies in the tensors outside the sequences (NaN included) does not reach them.
@@ -348,8 +353,9 @@ size_t fa2_bwd_varlen_workspace_size(int B, int T, int H, int Hkv, int d);
  *   Q, O, dO, dQ  : [T] x H heads; K, V, dK, dV : [T] x Hkv heads (dQ, dK, dV out)
  *   LSE           : in, [H][T] float, as fa2_fwd_varlen wrote it
  *   d             : a multiple of 8 up to 128
- *   workspace     : at least fa2_bwd_varlen_workspace_size() bytes, 256-byte aligned;
- *                   its contents on entry do not matter
+ *   workspace     : at least fa2_bwd_varlen_workspace_size() bytes, 256-byte aligned,
+ *                   not shared with a call that may run at the same time; its
+ *                   contents on entry do not matter
  * Other arguments as for the forward.  Rows behind the last sequence are left as they
  * were.  dQ may differ in the last bits from run to run (float atomics); dK and dV are
  * repeatable.
@@ -439,10 +445,12 @@ int fa2_paged_append(const fa2_packed* K, const fa2_packed* V, const fa2_cache* 
 /*
  * Synchronises ``stream``, then returns and clears the current device's status
  * words (the library's, and fa2_bwd_noalloc's if that call has run on the
- * device): FA2_OK, or FA2_ERR_TIMEOUT if a kernel gave up a bounded wait since the
- * last call (the kernel then skipped its output and exited cleanly; the CUDA
- * context stays usable).  FA2_ERR_CUDA if the synchronisation itself failed.
- * If ``site`` is not NULL it receives the id of the wait that ran out (0 if none).
+ * device): FA2_OK, or the first failure recorded since the last call --
+ * FA2_ERR_TIMEOUT if a kernel gave up a bounded wait (the kernel then skipped its
+ * output and exited cleanly; the CUDA context stays usable), FA2_ERR_INVALID_ARG if
+ * a paged call met a block or slot outside the cache.  FA2_ERR_CUDA if the
+ * synchronisation itself failed.  If ``site`` is not NULL it receives the id of the
+ * wait that ran out, or 120 for a block and 121 for a slot (0 if none).
  * Allocates nothing.  (``site`` is one argument more than a bare status query
  * needs; it tells which wait of which kernel ran out.)
  */
